@@ -29,6 +29,19 @@
  *   pyramid_verify       - PyramidSD fuzzy acceptance (lossy, behind its own entry point):
  *                          spec_verify where a position whose distributions are within a
  *                          divergence threshold keeps its drafted token outright.
+ *   spec_verify_probs    - the verification for callers that hold processed probabilities and
+ *                          draw their own random numbers.
+ *
+ * and the model-side steps of a round that scores drafted tokens, guessed outcomes and tree
+ * branches on top of one shared context:
+ *
+ *   spec_tree_rows        - the rows of draft trees: each node's position and the cache slots of
+ *                           the nodes above it.
+ *   spec_rope_frequencies - host helper: rotary inverse frequencies, scaled for long contexts.
+ *   spec_kv_append        - rotary positions for queries and keys, and the append of the keys and
+ *                           values to a paged cache.
+ *   spec_prefix_attention - attention of rows that share a long prefix of the paged cache and see
+ *                           tokens of their own behind it.
  *
  * Sources (notation p = draft, q = target, as on the DeepMind page):
  *   [SpS]   "Accelerating LLM Decoding with Speculative Sampling" (DeepMind, arXiv 2302.01318),
@@ -68,12 +81,14 @@ extern "C" {
 enum {
     SPEC_OK = 0,
     SPEC_EINVAL = -1,      /* null pointer, size < 1, F outside [0, SPEC_MAX_F], C outside [0, 1], ... */
-    SPEC_EDTYPE = -2,      /* dtype is neither SPEC_FP32 nor SPEC_BF16 */
-    SPEC_EWORKSPACE = -3,  /* workspace null or smaller than spec_workspace_bytes() */
+    SPEC_EDTYPE = -2,      /* dtype is none of those the entry point takes */
+    SPEC_EWORKSPACE = -3,  /* workspace null or smaller than its ..._workspace_bytes() */
     SPEC_EHIP = -4         /* a kernel launch failed (hipGetLastError after the launch) */
 };
 
-enum { SPEC_FP32 = 0, SPEC_BF16 = 1 };
+/* Element types.  The logit entry points take SPEC_FP32 and SPEC_BF16; the others say theirs.
+ * SPEC_E4M3: 8-bit floats of 4 exponent and 3 mantissa bits with no infinities (OCP e4m3fn). */
+enum { SPEC_FP32 = 0, SPEC_BF16 = 1, SPEC_FP16 = 2, SPEC_E4M3 = 3, SPEC_FP64 = 4 };
 
 #define SPEC_MAX_F 64          /* largest downweighted set */
 #define SPEC_MAX_FANOUT 1024   /* largest cache width for one depth */
@@ -104,9 +119,11 @@ enum {
                               temperature, top-k and top-p act on the target rows only; with
                               SPEC_SAMPLE_DRAFT, s_j = floor(u V) for the Philox lane-2 uniform u
                               (the inverse CDF of the uniform law, taken exactly) */
-    SPEC_ASSISTED = 4      /* pyramid_verify only: a rejected position draws its correction from
+    SPEC_ASSISTED = 4,     /* pyramid_verify only: a rejected position draws its correction from
                               the verifier's processed distribution q_j itself, not from the
                               residual ([PSD] key design 2, the assisted variant) */
+    SPEC_POINT_DRAFT = 8   /* spec_verify_probs only: every drafted token had probability 1 (a
+                              drafter that looks tokens up or takes its argmax) */
 };
 
 /* per-request status bits (out_status) */
@@ -120,10 +137,15 @@ enum {
     SPEC_ST_DEGENERATE_DOWNWEIGHT = 128,   /* C = 0 and the set holds all the draft mass: the
                                               row is left undownweighted */
     SPEC_ST_BAD_PARAM = 256,               /* invalid spec_params: k = 0, t* = -1 */
-    SPEC_ST_PLACEMENT = 512                /* the exact-count path found the workgroups of one
+    SPEC_ST_PLACEMENT = 512,               /* the exact-count path found the workgroups of one
                                               position on different XCDs (its slices meet in one
                                               XCD's L2): the request was redone by the general
                                               path.  Never expected; a guard on the launch map */
+    SPEC_ST_BAD_PROB = 1024,               /* spec_verify_probs: a negative, infinite or NaN
+                                              probability where one was read, or a target row
+                                              without mass: k = 0, t* = -1 */
+    SPEC_ST_BAD_SLOT = 2048                /* spec_kv_append: a slot past the cache (nothing of
+                                              that token was stored) */
 };
 
 /* Uniforms.  Counter-based Philox4x64-10 (Salmon et al., SC'11) with key (seed, 0) and counter
@@ -365,6 +387,168 @@ int saguaro_verify_cache_lookup_timed(const void* draft_logits, const void* targ
                                       int32_t* out_slot, uint8_t* out_hit, int32_t* out_batch, void* workspace,
                                       size_t workspace_bytes, hipStream_t stream, hipEvent_t count_before,
                                       hipEvent_t count_after);
+
+/* ---------------------------------------------------------------------------------------------
+ * Verification from given probabilities
+ * ------------------------------------------------------------------------------------------- */
+
+/* Bytes of scratch spec_verify_probs needs for B requests over V tokens (pure host function; 0
+ * for sizes it rejects).  Every call writes what it reads of it, so it needs no clearing; one
+ * workspace serves one call at a time (two captured graphs that may run at once need two). */
+size_t spec_verify_probs_workspace_bytes(int B, int V);
+
+/* spec_verify_probs - the acceptance scan and the correction token of spec_verify ([SpS]
+ * sections 1 and 3) for callers that hold processed probabilities and draw their own random
+ * numbers.  For each request b with L = draft_lens[b] drafted tokens (K where draft_lens is null):
+ *   for j = 0..L-1: accept s_j iff u_j * p_j(s_j) < q_j(s_j) (in fp64); stop at the first
+ *   rejection; k = number of accepted tokens.  k < L: t* ~ (q_k - p_k)+ ; k = L: t* ~ q_L.
+ *   t* is the first token whose running mass exceeds v times the row's total, and the last one
+ *   that has mass where none does (v = 1).  Rows need not sum to 1: each is taken over its own
+ *   total.  Masses are summed in fp64.  A rejection that leaves no residual draws from q_k.
+ *   draft_probs   [B][K][V], or null with SPEC_UNIFORM_DRAFT (p = 1/V everywhere) or
+ *                 SPEC_POINT_DRAFT (p = 1 at the drafted token)
+ *   target_probs  [B][K+1][V] (rows past L are not read)
+ *   dtype         SPEC_FP32, SPEC_BF16 or SPEC_FP16, of both
+ *   *_request_stride, *_row_stride   in elements; V is contiguous.  No alignment is needed
+ *                 beyond the element's
+ *   draft_tokens  [B][K] int32; entries past L are not read
+ *   draft_lens    [B] int32 in [0, K] (nullable)
+ *   accept_u      [B][K], sample_v [B], in [0, 1]; uniform_dtype SPEC_FP32 or SPEC_FP64
+ *   flags         0, SPEC_UNIFORM_DRAFT or SPEC_POINT_DRAFT
+ *   out_k, out_tstar [B] int32; out_emitted [B][K+1] int32 (nullable): the accepted tokens, then
+ *                 t*, then -1; out_resid_mass [B] float (nullable); out_status [B] (nullable)
+ * Status: SPEC_ST_EMPTY_RESIDUAL, _OUTSIDE_DRAFT_SUPPORT, and with k = 0, t* = -1: _BAD_PROB
+ * (among the probabilities read), _BAD_TOKEN (a drafted token that the scan reached), _BAD_PARAM
+ * (a length outside [0, K], a random number that was used and is outside [0, 1] or NaN).
+ * One launch for up to 8192 tokens, otherwise two. */
+int spec_verify_probs(const void* draft_probs, int64_t draft_request_stride, int64_t draft_row_stride,
+                      const void* target_probs, int64_t target_request_stride, int64_t target_row_stride, int dtype,
+                      int B, int K, int V, const int32_t* draft_tokens, const int32_t* draft_lens, const void* accept_u,
+                      const void* sample_v, int uniform_dtype, uint32_t flags, int32_t* out_k, int32_t* out_tstar,
+                      int32_t* out_emitted, float* out_resid_mass, uint32_t* out_status, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Draft-tree rows, the paged cache and attention over a shared prefix
+ * ------------------------------------------------------------------------------------------- */
+
+/* spec_tree_rows - the rows that score a draft tree in one pass of a model ([MSD] section 3.1:
+ * the branches hang off one context; [SSD] section 5.1: guessed outcomes hang off the drafted
+ * chain).  Trees as in mirror_tree_lookup: N nodes per request, parents first,
+ * tree_parents[b][n] in [-1, n) (-1: it follows the context), a node with a negative token or
+ * another parent is not part of the tree, nor is anything below it, nor is a node deeper than
+ * max_depth.  A chain is the tree with parents n - 1.
+ *   node_slots        [B][N] int32: the cache slot each node's key and value go to
+ *   ctx_len           [B] int32: tokens already in the context
+ *   max_depth         entries per list (>= 1)
+ *   out_positions     [B][N] int32: ctx_len + depth - 1 for a node of depth 1 (a root), 2, ...;
+ *                     -1 for a node outside the tree
+ *   out_append_slots  [B][N] int32: node_slots, -1 for a node outside the tree
+ *   out_suffix_slots  [B][N][max_depth] int32: the slots from the root to the node, then -1
+ *   out_suffix_len    [B][N] int32: the depth; 0 for a node outside the tree
+ * positions and append_slots feed spec_kv_append, the lists spec_prefix_attention. */
+int spec_tree_rows(const int32_t* tree_tokens, const int32_t* tree_parents, const int32_t* node_slots,
+                   const int32_t* ctx_len, int B, int N, int max_depth, int32_t* out_positions,
+                   int32_t* out_append_slots, int32_t* out_suffix_slots, int32_t* out_suffix_len, hipStream_t stream);
+
+/* A paged cache of keys and values: k and v are [num_pages][page_size][heads][head_dim] with
+ * head_dim contiguous and the other strides in elements, the same for both (so a cache with heads
+ * outside tokens, or keys and values side by side in one buffer, is described as well).  Slot s is
+ * token s % page_size of page s / page_size; num_pages * page_size < 2^31.
+ * dtype SPEC_BF16, SPEC_FP16, or SPEC_E4M3 with k_scale and v_scale [heads] float (null: 1): the
+ * key of head h is its 8-bit value times k_scale[h]. */
+typedef struct {
+    void* k;
+    void* v;
+    int32_t dtype;
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t heads;
+    int32_t head_dim;
+    int64_t page_stride;
+    int64_t token_stride;
+    int64_t head_stride;
+    const float* k_scale;
+    const float* v_scale;
+} spec_kv_cache;
+
+/* Host helper: rotary inverse frequencies f_i = base^(-2i / rot_dim), i < rot_dim / 2, with those
+ * that turn slowly stretched for a context `factor` times the original one: with
+ * n_i = original_len f_i / 2 pi turns over the original context and
+ * g_i = clamp((n_i - low) / (high - low), 0, 1), f_i becomes f_i (g_i + (1 - g_i) / factor).
+ * factor = 1 leaves all as they are; low = high takes g_i = (n_i >= low) (+inf: all stretched,
+ * linear interpolation of positions).  rot_dim even and >= 2, base > 0, factor >= 1, low <= high,
+ * original_len >= 1.  out [rot_dim / 2] host. */
+int spec_rope_frequencies(int rot_dim, double base, double factor, double low, double high, int original_len,
+                          double* out);
+
+enum { SPEC_ROPE_INTERLEAVED = 1 }; /* pairs (2i, 2i + 1); without it pairs (i, i + rot_dim / 2) */
+
+/* spec_kv_append - rotary positions and the append to the paged cache in one pass: queries are
+ * rotated into q_out, keys are rotated on their way into the cache, values go along.
+ * The pair (x, y) of index i becomes rope_scale * (x cos - y sin, y cos + x sin) with the angle
+ * position * freqs[i] taken in fp64; elements from rot_dim on pass through.  Sums are in fp32 and
+ * rounded once, to the output's type; an 8-bit cache holds (value / scale), clamped to its range.
+ *   q        [T][q_heads][head_dim] (null: no queries), q_out likewise: q itself (in place, the
+ *            same strides) or memory apart from it
+ *   k, v     [T][heads][head_dim] (both null with a null cache: queries only)
+ *   dtype    SPEC_BF16 or SPEC_FP16, of q, q_out, k and v; a cache of that type or SPEC_E4M3
+ *   strides  in elements, per token and per head; head_dim is contiguous
+ *   positions [T] int32;  freqs [rot_dim / 2] double, device; rot_dim even, 0 (no rotation, freqs
+ *            and positions may be null) to head_dim;  rope_scale: a factor on cos and sin (1: none)
+ *   slots    [T] int32: -1 stores nothing for that token (its query is rotated all the same).
+ *            Slots of one call differ; where two are the same, which of the values stays is open
+ *   out_status [T] (nullable): SPEC_ST_BAD_SLOT for a slot outside [-1, num_pages * page_size),
+ *            which stores nothing, else 0
+ * T = 0 launches nothing.  Rows of eight elements that start 16-byte aligned move as vectors;
+ * other strides and sizes are taken element by element. */
+int spec_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out, int64_t q_out_token_stride,
+                   int64_t q_out_head_stride, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                   const void* v, int64_t v_token_stride, int64_t v_head_stride, int dtype, int T, int q_heads,
+                   int heads, int head_dim, const int32_t* positions, const int32_t* slots, const double* freqs,
+                   int rot_dim, float rope_scale, uint32_t rope_flags, const spec_kv_cache* cache, uint32_t* out_status,
+                   hipStream_t stream);
+
+/* Bytes of scratch spec_prefix_attention needs (pure host function; 0 for sizes it rejects):
+ * rows R, groups G, query heads, cache heads, head_dim, and the longest prefix the page table can
+ * hold (max_pages * page_size).  Every call writes what it reads of it, so it needs no clearing;
+ * one workspace serves one call at a time (two captured graphs that may run at once need two). */
+size_t spec_prefix_attention_workspace_bytes(int R, int G, int q_heads, int heads, int head_dim,
+                                             int64_t max_prefix);
+
+/* spec_prefix_attention - attention of R rows (one query token each) in G groups: the rows of a
+ * group share a prefix of the cache and see tokens of their own behind it ([SSD] section 8.2,
+ * [MSD] section 3.1: all branches of a request are scored on one context).  The keys and values of
+ * a prefix are read once for all rows of its group.  For row r of group g and query head h, with
+ * cache head h / (q_heads / heads):
+ *   out[r][h] = sum_t softmax_t(scale * q[r][h] . k_t) v_t
+ * over the prefix tokens t < prefix_len[g] (slot page_table[g][t / page_size] * page_size +
+ * t % page_size) and the tokens at the slots suffix_slots[r][i], i < suffix_len[r].
+ * Rows verify, decode and roll out alike: a chain's token j lists the chain's slots 0..j, a tree
+ * node the slots from its root (spec_tree_rows), a plain decoding step its own slot or none.
+ *   q, out       [R][q_heads][head_dim], dtype SPEC_BF16 or SPEC_FP16; strides in elements per row
+ *                and per head, head_dim contiguous
+ *   cache        of q's dtype or SPEC_E4M3; q_heads a multiple of cache heads
+ *   row_start    [G+1] int32, not decreasing, in [0, R]: group g holds rows row_start[g] to
+ *                row_start[g+1] - 1.  Rows outside every group (padding) are left as they were
+ *   page_table   [G][max_pages] int32;  prefix_len [G] int32 (taken within [0, max_pages *
+ *                page_size]).  max_pages may be 0 (then both may be null)
+ *   suffix_slots [R][max_suffix] int32, suffix_len [R] int32 (taken within [0, max_suffix]);
+ *                max_suffix may be 0 (then both may be null)
+ *   out_lse      [R][q_heads] float (nullable): log of the sum of exp of the scaled scores
+ * A page outside [0, num_pages) and a slot outside the cache hold no token: they are left out, as
+ * holes of a mask.  A row that sees nothing (or only scores of -inf) gives zeros and lse = -inf.
+ * What lies in the cache outside the tokens named does not matter, NaN and infinities included.
+ * Scores, softmax statistics and sums are in fp32; the weights are rounded to q's type for the
+ * product with the values.
+ * R = 0 launches nothing.  head_dim: a multiple of 8, up to 256.  out is apart from q.  q, out, k and v 16-byte aligned (k and v of an 8-bit
+ * cache 8-byte), strides multiples of 8 elements: otherwise SPEC_EINVAL. */
+int spec_prefix_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride, int dtype, int R, int q_heads,
+                          const spec_kv_cache* cache, int G, const int32_t* row_start, const int32_t* page_table,
+                          int max_pages, const int32_t* prefix_len, const int32_t* suffix_slots, int max_suffix,
+                          const int32_t* suffix_len, float scale, void* out, int64_t out_row_stride,
+                          int64_t out_head_stride, float* out_lse, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream);
 
 /* spec_read_ceiling - measurement helper, not part of the method: one plain streaming read of
  * `bytes` bytes of device memory at `data` (16-byte aligned, bytes a multiple of 16), the

@@ -17,10 +17,12 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libspecverify.so")
 
 SPEC_OK, SPEC_EINVAL, SPEC_EDTYPE, SPEC_EWORKSPACE, SPEC_EHIP = 0, -1, -2, -3, -4
-SPEC_FP32, SPEC_BF16 = 0, 1
+SPEC_FP32, SPEC_BF16, SPEC_FP16, SPEC_E4M3, SPEC_FP64 = 0, 1, 2, 3, 4
 SPEC_SAMPLE_DRAFT = 1
 SPEC_UNIFORM_DRAFT = 2
 SPEC_ASSISTED = 4
+SPEC_POINT_DRAFT = 8
+SPEC_ROPE_INTERLEAVED = 1
 SPEC_MAX_F = 64
 SPEC_MAX_KAPPA = 16
 SPEC_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -31,16 +33,29 @@ ST_BAD_TOKEN = 64
 ST_DEGENERATE_DOWNWEIGHT = 128
 ST_BAD_PARAM = 256
 ST_PLACEMENT = 512
+ST_BAD_PROB = 1024
+ST_BAD_SLOT = 2048
 
 EXPORTS = ("spec_workspace_bytes", "spec_verify", "saguaro_downweight", "saguaro_fanout", "saguaro_cache_build",
            "saguaro_cache_lookup", "saguaro_verify_cache", "saguaro_backup_plan", "mirror_signpost_workspace_bytes",
            "mirror_signposts", "mirror_tree_lookup", "pyramid_verify", "spec_read_ceiling",
-           "saguaro_verify_cache_noalloc", "saguaro_verify_cache_lookup", "saguaro_verify_cache_lookup_timed")
+           "saguaro_verify_cache_noalloc", "saguaro_verify_cache_lookup", "saguaro_verify_cache_lookup_timed",
+           "spec_verify_probs_workspace_bytes", "spec_verify_probs", "spec_tree_rows", "spec_rope_frequencies",
+           "spec_kv_append", "spec_prefix_attention_workspace_bytes", "spec_prefix_attention")
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _U64 = ctypes.c_uint64
+_I64 = ctypes.c_int64
 _D = ctypes.c_double
+_F = ctypes.c_float
+
+
+class _Cache(ctypes.Structure):
+    """spec_kv_cache of the C ABI."""
+    _fields_ = [("k", _P), ("v", _P), ("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_stride", _I64), ("token_stride", _I64), ("head_stride", _I64), ("k_scale", _P), ("v_scale", _P)]
 
 
 class SpecError(RuntimeError):
@@ -81,8 +96,20 @@ class Lib:
         L.saguaro_verify_cache_lookup_timed.argtypes = L.saguaro_verify_cache_lookup.argtypes + [_P, _P]
         L.saguaro_verify_cache_noalloc.argtypes = [_P, _P, _I, _I, _I, _I, _P, _I, ctypes.c_float, _P, _U64, _U64,
                                                    ctypes.c_uint32, _I, _D, _D, _P, _P, _P, _P, _P, _P, _P]
+        L.spec_verify_probs.argtypes = [_P, _I64, _I64, _P, _I64, _I64, _I, _I, _I, _I, _P, _P, _P, _P, _I,
+                                        ctypes.c_uint32, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
+        L.spec_tree_rows.argtypes = [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P]
+        L.spec_rope_frequencies.argtypes = [_I, _D, _D, _D, _D, _I, _P]
+        L.spec_kv_append.argtypes = [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I, _I, _I, _I, _I,
+                                     _P, _P, _P, _I, _F, ctypes.c_uint32, _P, _P, _P]
+        L.spec_prefix_attention.argtypes = [_P, _I64, _I64, _I, _I, _I, _P, _I, _P, _P, _I, _P, _P, _I, _P, _F, _P,
+                                            _I64, _I64, _P, _P, ctypes.c_size_t, _P]
         for fn in EXPORTS[1:]:
             getattr(L, fn).restype = _I
+        L.spec_verify_probs_workspace_bytes.argtypes = [_I, _I]
+        L.spec_prefix_attention_workspace_bytes.argtypes = [_I, _I, _I, _I, _I, _I64]
+        for fn in ("spec_verify_probs_workspace_bytes", "spec_prefix_attention_workspace_bytes"):
+            getattr(L, fn).restype = ctypes.c_size_t
 
 
 _lib: Optional[Lib] = None
@@ -477,6 +504,301 @@ def pyramid_verify(draft: Optional[torch.Tensor], verifier: torch.Tensor, K: int
                                     _ptr(workspace), workspace.numel(), _stream(stream))
     _check("pyramid_verify", rc)
     return out, div
+
+
+# ---- the steps on either side of the verification.  These take strided tensors where the C ABI has
+# strides, and run on the device of their tensors (its current stream unless `stream` is given),
+# whichever device is current. ----
+_HALF = {torch.bfloat16: SPEC_BF16, torch.float16: SPEC_FP16}
+_PROBS = {torch.float32: SPEC_FP32, **_HALF}
+
+
+def _same_device(**tensors) -> torch.device:
+    """The one GPU that every given tensor lies on."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        _need(t.is_cuda, f"{name}: device tensor expected")
+        dev = t.device if dev is None else dev
+        _need(t.device == dev, f"{name} lies on {t.device}, the others on {dev}")
+    return dev
+
+
+def _whole(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple):
+    _need(t is not None, f"{name} is required")
+    _need(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
+    _need(t.shape == torch.Size(shape), f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _need(t.is_contiguous(), f"{name} must be contiguous")
+
+
+def _inner(name: str, t: torch.Tensor):
+    _need(t.stride(-1) == 1 or t.shape[-1] == 1, f"{name}: the last dimension must be contiguous")
+
+
+def _call(fn: str, dev: torch.device, stream, *args):
+    """Calls the library with the stream last, on `dev`."""
+    if dev.index == torch.cuda.current_device():
+        rc = getattr(load().cdll, fn)(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(load().cdll, fn)(*args, _stream(stream))
+    if rc != SPEC_OK:
+        raise SpecError(fn, rc)
+
+
+def _data(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+@dataclass
+class ProbsOut:
+    k: torch.Tensor           # [B] int32
+    tstar: torch.Tensor       # [B] int32
+    emitted: torch.Tensor     # [B][K+1] int32: accepted tokens, t*, then -1
+    resid_mass: torch.Tensor  # [B] float32
+    status: torch.Tensor      # [B] int32 status bits
+
+
+def spec_verify_probs_workspace_bytes(B: int, V: int) -> int:
+    return int(load().cdll.spec_verify_probs_workspace_bytes(B, V))
+
+
+def spec_verify_probs(draft: Optional[torch.Tensor], target: torch.Tensor, tokens: torch.Tensor, accept_u: torch.Tensor,
+                      sample_v: torch.Tensor, draft_lens: Optional[torch.Tensor] = None, flags: int = 0,
+                      workspace: Optional[torch.Tensor] = None, out: Optional[ProbsOut] = None, stream=None) -> ProbsOut:
+    """Verification from given probabilities, draft [B][K][V] (None with SPEC_UNIFORM_DRAFT or
+    SPEC_POINT_DRAFT) and target [B][K+1][V] in fp32, bf16 or fp16, and given random numbers accept_u
+    [B][K] and sample_v [B] in fp32 or fp64; tokens [B][K] and draft_lens [B] int32."""
+    _need(target.dim() == 3 and target.dtype in _PROBS, "target must be [B][K+1][V] in fp32, bf16 or fp16")
+    B, rows, V = target.shape
+    K = rows - 1
+    _need(B >= 1 and K >= 1 and V >= 1, f"target {tuple(target.shape)} holds no drafted position")
+    _inner("target", target)
+    if draft is None:
+        _need(flags != 0, "draft probabilities are required without SPEC_UNIFORM_DRAFT or SPEC_POINT_DRAFT")
+        ds = (0, 0)
+    else:
+        _need(draft.dtype == target.dtype, "draft and target must have the same dtype")
+        _need(draft.shape == (B, K, V), f"draft must be {(B, K, V)}, got {tuple(draft.shape)}")
+        _inner("draft", draft)
+        ds = (draft.stride(0), draft.stride(1))
+    _whole("tokens", tokens, torch.int32, (B, K))
+    _need(accept_u.dtype in (torch.float32, torch.float64), "accept_u must be float32 or float64")
+    _whole("accept_u", accept_u, accept_u.dtype, (B, K))
+    _whole("sample_v", sample_v, accept_u.dtype, (B,))
+    if draft_lens is not None:
+        _whole("draft_lens", draft_lens, torch.int32, (B,))
+    dev = target.device
+    if out is None:
+        ints = torch.empty(B * (K + 5), dtype=torch.int32, device=dev)
+        out = ProbsOut(ints[:B], ints[B:2 * B], ints[4 * B:].view(B, K + 1), ints[3 * B:4 * B].view(torch.float32),
+                       ints[2 * B:3 * B])
+    else:
+        for name, shape in (("k", (B,)), ("tstar", (B,)), ("emitted", (B, K + 1)), ("status", (B,))):
+            _whole(f"out.{name}", getattr(out, name), torch.int32, shape)
+        _whole("out.resid_mass", out.resid_mass, torch.float32, (B,))
+    if workspace is None:
+        workspace = torch.empty(max(spec_verify_probs_workspace_bytes(B, V), 1), dtype=torch.uint8, device=dev)
+    _workspace(workspace)
+    _same_device(target=target, draft=draft, tokens=tokens, accept_u=accept_u, sample_v=sample_v, draft_lens=draft_lens,
+                 out=out.k, emitted=out.emitted, workspace=workspace)
+    _call("spec_verify_probs", dev, stream, _data(draft), *ds, _data(target), target.stride(0), target.stride(1),
+          _PROBS[target.dtype], B, K, V, _data(tokens), _data(draft_lens), _data(accept_u), _data(sample_v),
+          SPEC_FP64 if accept_u.dtype == torch.float64 else SPEC_FP32, flags, _data(out.k), _data(out.tstar),
+          _data(out.emitted), _data(out.resid_mass), _data(out.status), _data(workspace), workspace.numel())
+    return out
+
+
+@dataclass
+class TreeRows:
+    positions: torch.Tensor     # [B][N] int32, -1 outside the tree
+    append_slots: torch.Tensor  # [B][N] int32, -1 outside the tree
+    suffix_slots: torch.Tensor  # [B][N][max_depth] int32, root to node, then -1
+    suffix_len: torch.Tensor    # [B][N] int32: the depth, 0 outside the tree
+
+
+def spec_tree_rows(tokens: torch.Tensor, parents: torch.Tensor, slots: torch.Tensor, ctx_len: torch.Tensor,
+                   max_depth: int, out: Optional[TreeRows] = None, stream=None) -> TreeRows:
+    """The rows of draft trees [B][N] (parents first, as in mirror_tree_lookup) on contexts of ctx_len [B]
+    tokens, node n of request b at cache slot slots[b][n]."""
+    _need(tokens.dim() == 2, "tokens must be [B][N]")
+    B, N = tokens.shape
+    _whole("tokens", tokens, torch.int32, (B, N))
+    _whole("parents", parents, torch.int32, (B, N))
+    _whole("slots", slots, torch.int32, (B, N))
+    _whole("ctx_len", ctx_len, torch.int32, (B,))
+    _need(max_depth >= 1, "max_depth must be at least 1")
+    dev = tokens.device
+    if out is None:
+        ints = torch.empty(B * N * (max_depth + 3), dtype=torch.int32, device=dev)
+        n = B * N
+        out = TreeRows(ints[:n].view(B, N), ints[n:2 * n].view(B, N), ints[3 * n:].view(B, N, max_depth),
+                       ints[2 * n:3 * n].view(B, N))
+    else:
+        for name in ("positions", "append_slots", "suffix_len"):
+            _whole(f"out.{name}", getattr(out, name), torch.int32, (B, N))
+        _whole("out.suffix_slots", out.suffix_slots, torch.int32, (B, N, max_depth))
+    _same_device(tokens=tokens, parents=parents, slots=slots, ctx_len=ctx_len, out=out.suffix_slots,
+                 positions=out.positions)
+    _call("spec_tree_rows", dev, stream, _data(tokens), _data(parents), _data(slots), _data(ctx_len), B, N, max_depth,
+          _data(out.positions), _data(out.append_slots), _data(out.suffix_slots), _data(out.suffix_len))
+    return out
+
+
+def spec_rope_frequencies(rot_dim: int, base: float = 10000.0, factor: float = 1.0, low: float = 1.0, high: float = 4.0,
+                          original_len: int = 8192) -> list[float]:
+    """Rotary inverse frequencies, those that turn slowly stretched by `factor` (1: none)."""
+    buf = (ctypes.c_double * max(rot_dim // 2, 1))()
+    _check("spec_rope_frequencies", load().cdll.spec_rope_frequencies(rot_dim, base, factor, low, high, original_len,
+                                                                      ctypes.cast(buf, _P)))
+    return list(buf)
+
+
+@dataclass
+class Rotary:
+    freqs: torch.Tensor        # [rot_dim / 2] float64 on the device
+    interleaved: bool = False  # pairs (2i, 2i + 1); otherwise (i, i + rot_dim / 2)
+    scale: float = 1.0         # a factor on cos and sin
+
+
+@dataclass
+class KVCache:
+    """A paged cache: k and v [num_pages][page_size][heads][head_dim], bf16, fp16 or float8_e4m3fn (with
+    float32 scales [heads], None: 1); slot s is token s % page_size of page s // page_size.  Views with
+    other strides will do, the same for k and v, as long as head_dim is contiguous."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: Optional[torch.Tensor] = None
+    v_scale: Optional[torch.Tensor] = None
+
+    def described(self) -> _Cache:
+        k, v = self.k, self.v
+        _need(k.dim() == 4 and k.shape == v.shape, "cache: k and v must be [num_pages][page_size][heads][head_dim] alike")
+        _need(k.dtype == v.dtype, "cache: k and v must have the same dtype")
+        _need(k.stride() == v.stride(), "cache: k and v must have the same strides")
+        _need(k.stride(3) == 1 or k.shape[3] == 1, "cache: head_dim must be contiguous")
+        eight = k.dtype == torch.float8_e4m3fn
+        _need(eight or k.dtype in _HALF, f"cache: unsupported dtype {k.dtype}")
+        for name, x in (("k_scale", self.k_scale), ("v_scale", self.v_scale)):
+            if x is not None:
+                _need(eight, f"cache: {name} belongs to an 8-bit cache")
+                _whole(f"cache.{name}", x, torch.float32, (k.shape[2],))
+        pages, page, heads, dim = k.shape
+        ps, ts, hs, _ = k.stride()
+        return _Cache(k.data_ptr(), v.data_ptr(), SPEC_E4M3 if eight else _HALF[k.dtype], pages, page, heads, dim, ps, ts,
+                      hs, _data(self.k_scale), _data(self.v_scale))
+
+
+def spec_kv_append(k: Optional[torch.Tensor], v: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                   slots: Optional[torch.Tensor], cache: Optional[KVCache], rotary: Optional[Rotary] = None,
+                   q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Rotates k [T][heads][head_dim] and stores it with v into the cache at slots [T] (int32, -1: none), and
+    rotates q [T][q_heads][head_dim] into q_out (allocated here unless given; q itself: in place), which is
+    returned.  k, v, slots and cache may all be None (queries only), and q (keys and values only)."""
+    lead = q if q is not None else k
+    _need(lead is not None and lead.dim() == 3, "q or k must be given, as [T][heads][head_dim]")
+    _need((k is None) == (v is None) == (cache is None) and (k is None or slots is not None),
+          "k, v, slots and cache come together")
+    T, _, D = lead.shape
+    _need(lead.dtype in _HALF, f"unsupported dtype {lead.dtype}")
+    desc, kst, heads = None, (0, 0, 0, 0), 0
+    if k is not None:
+        heads = k.shape[1]
+        _need(v.shape == k.shape, "k and v must have the same shape")
+        _need(k.dim() == 3 and k.shape[0] == T and k.shape[2] == D, f"k must be [{T}][heads][{D}], got {tuple(k.shape)}")
+        _need(k.dtype == lead.dtype and v.dtype == lead.dtype, "q, k and v must have the same dtype")
+        _inner("k", k)
+        _inner("v", v)
+        _whole("slots", slots, torch.int32, (T,))
+        desc = cache.described()
+        _need((desc.heads, desc.head_dim) == (heads, D), f"cache heads {(desc.heads, desc.head_dim)} do not match k {(heads, D)}")
+        kst = (k.stride(0), k.stride(1), v.stride(0), v.stride(1))
+    q_heads, qst, ost = 0, (0, 0), (0, 0)
+    if q is not None:
+        q_heads = q.shape[1]
+        _inner("q", q)
+        if q_out is None:
+            q_out = torch.empty((T, q_heads, D), dtype=q.dtype, device=q.device)
+        _need(q_out.shape == q.shape and q_out.dtype == q.dtype, "q_out must be like q")
+        _inner("q_out", q_out)
+        qst, ost = q.stride()[:2], q_out.stride()[:2]
+    rot, rscale, rflags, freqs = 0, 1.0, 0, None
+    if rotary is not None:
+        freqs = rotary.freqs
+        _need(freqs.dim() == 1 and 2 * freqs.numel() <= D, f"rotary.freqs must hold at most {D // 2} frequencies")
+        _whole("rotary.freqs", freqs, torch.float64, (freqs.numel(),))
+        _whole("positions", positions, torch.int32, (T,))
+        rot, rscale, rflags = 2 * freqs.numel(), rotary.scale, SPEC_ROPE_INTERLEAVED if rotary.interleaved else 0
+    if status is not None:
+        _whole("status", status, torch.int32, (T,))
+    dev = _same_device(q=q, q_out=q_out if q is not None else None, k=k, v=v, positions=positions if rot else None,
+                       slots=slots if k is not None else None, freqs=freqs, status=status,
+                       cache=cache.k if cache else None, cache_v=cache.v if cache else None,
+                       k_scale=cache.k_scale if cache else None, v_scale=cache.v_scale if cache else None)
+    _call("spec_kv_append", dev, stream, _data(q), *qst, _data(q_out) if q is not None else None, *ost, _data(k), *kst[:2],
+          _data(v), *kst[2:], _HALF[lead.dtype], T, q_heads, heads, D, _data(positions) if rot else None,
+          _data(slots) if k is not None else None, _data(freqs), rot, rscale, rflags,
+          ctypes.byref(desc) if desc else None, _data(status))
+    return q_out if q is not None else None
+
+
+def spec_prefix_attention_workspace_bytes(R: int, G: int, q_heads: int, heads: int, head_dim: int,
+                                          max_prefix: int) -> int:
+    return int(load().cdll.spec_prefix_attention_workspace_bytes(R, G, q_heads, heads, head_dim, max_prefix))
+
+
+def spec_prefix_attention(q: torch.Tensor, cache: KVCache, page_table: Optional[torch.Tensor],
+                          prefix_len: Optional[torch.Tensor], row_start: torch.Tensor,
+                          suffix_slots: Optional[torch.Tensor] = None, suffix_len: Optional[torch.Tensor] = None,
+                          scale: Optional[float] = None, out: Optional[torch.Tensor] = None, want_lse: bool = False,
+                          lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of rows q [R][q_heads][head_dim] in groups row_start [G+1], each over its group's prefix
+    (page_table [G][max_pages], prefix_len [G]) and its own suffix_slots [R][max_suffix], suffix_len [R].  scale:
+    head_dim^-0.5 unless given.  Returns (out, lse); lse [R][q_heads] float32 with want_lse, else None.  Rows
+    outside every group (padding) keep what out and lse held, so give both where there are such rows."""
+    _need(q.dim() == 3 and q.dtype in _HALF, "q must be [R][q_heads][head_dim] in bf16 or fp16")
+    R, Hq, D = q.shape
+    _inner("q", q)
+    desc = cache.described()
+    _need(desc.head_dim == D and desc.heads >= 1 and Hq % desc.heads == 0,
+          f"cache heads {(desc.heads, desc.head_dim)} do not serve q {(Hq, D)}")
+    _need(row_start.dim() == 1 and row_start.numel() >= 2, "row_start must be [G+1]")
+    G = row_start.numel() - 1
+    _whole("row_start", row_start, torch.int32, (G + 1,))
+    pages = S = 0
+    if page_table is not None:
+        _need(page_table.dim() == 2, "page_table must be [G][max_pages]")
+        pages = page_table.shape[1]
+        _whole("page_table", page_table, torch.int32, (G, pages))
+        _whole("prefix_len", prefix_len, torch.int32, (G,))
+    if suffix_slots is not None:
+        _need(suffix_slots.dim() == 2, "suffix_slots must be [R][max_suffix]")
+        S = suffix_slots.shape[1]
+        _whole("suffix_slots", suffix_slots, torch.int32, (R, S))
+        _whole("suffix_len", suffix_len, torch.int32, (R,))
+    dev = q.device
+    if out is None:
+        out = torch.empty((R, Hq, D), dtype=q.dtype, device=dev)
+    _need(out.shape == q.shape and out.dtype == q.dtype, "out must be like q")
+    _inner("out", out)
+    if lse is None and want_lse:
+        lse = torch.empty((R, Hq), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _whole("lse", lse, torch.float32, (R, Hq))
+    if workspace is None:
+        workspace = torch.empty(max(spec_prefix_attention_workspace_bytes(R, G, Hq, desc.heads, D, pages * desc.page_size), 1),
+                                dtype=torch.uint8, device=dev)
+    _workspace(workspace)
+    _same_device(q=q, cache=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale, page_table=page_table,
+                 prefix_len=prefix_len, row_start=row_start, suffix_slots=suffix_slots, suffix_len=suffix_len, out=out,
+                 lse=lse, workspace=workspace)
+    _call("spec_prefix_attention", dev, stream, _data(q), q.stride(0), q.stride(1), _HALF[q.dtype], R, Hq,
+          ctypes.byref(desc), G, _data(row_start), _data(page_table), pages, _data(prefix_len), _data(suffix_slots), S,
+          _data(suffix_len), D ** -0.5 if scale is None else scale, _data(out), out.stride(0), out.stride(1), _data(lse),
+          _data(workspace), workspace.numel())
+    return out, lse
 
 
 def spec_read_ceiling(data: torch.Tensor, sink: torch.Tensor, stream: Optional[int] = None) -> None:
