@@ -510,11 +510,11 @@ int spec_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                    hipStream_t stream);
 
 /* Bytes of scratch spec_prefix_attention needs (pure host function; 0 for sizes it rejects):
- * rows R, groups G, query heads, cache heads, head_dim, and the longest prefix the page table can
- * hold (max_pages * page_size).  Every call writes what it reads of it, so it needs no clearing;
+ * rows R, groups G, query heads, cache heads, head_dim, the longest prefix the page table can hold
+ * (max_pages * page_size), and the entries of a suffix list.  Every call writes what it reads of it, so it needs no clearing;
  * one workspace serves one call at a time (two captured graphs that may run at once need two). */
 size_t spec_prefix_attention_workspace_bytes(int R, int G, int q_heads, int heads, int head_dim,
-                                             int64_t max_prefix);
+                                             int64_t max_prefix, int max_suffix);
 
 /* spec_prefix_attention - attention of R rows (one query token each) in G groups: the rows of a
  * group share a prefix of the cache and see tokens of their own behind it ([SSD] section 8.2,

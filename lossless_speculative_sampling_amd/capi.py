@@ -107,7 +107,7 @@ class Lib:
         for fn in EXPORTS[1:]:
             getattr(L, fn).restype = _I
         L.spec_verify_probs_workspace_bytes.argtypes = [_I, _I]
-        L.spec_prefix_attention_workspace_bytes.argtypes = [_I, _I, _I, _I, _I, _I64]
+        L.spec_prefix_attention_workspace_bytes.argtypes = [_I, _I, _I, _I, _I, _I64, _I]
         for fn in ("spec_verify_probs_workspace_bytes", "spec_prefix_attention_workspace_bytes"):
             getattr(L, fn).restype = ctypes.c_size_t
 
@@ -745,8 +745,8 @@ def spec_kv_append(k: Optional[torch.Tensor], v: Optional[torch.Tensor], positio
 
 
 def spec_prefix_attention_workspace_bytes(R: int, G: int, q_heads: int, heads: int, head_dim: int,
-                                          max_prefix: int) -> int:
-    return int(load().cdll.spec_prefix_attention_workspace_bytes(R, G, q_heads, heads, head_dim, max_prefix))
+                                          max_prefix: int, max_suffix: int) -> int:
+    return int(load().cdll.spec_prefix_attention_workspace_bytes(R, G, q_heads, heads, head_dim, max_prefix, max_suffix))
 
 
 def spec_prefix_attention(q: torch.Tensor, cache: KVCache, page_table: Optional[torch.Tensor],
@@ -788,7 +788,7 @@ def spec_prefix_attention(q: torch.Tensor, cache: KVCache, page_table: Optional[
     if lse is not None:
         _whole("lse", lse, torch.float32, (R, Hq))
     if workspace is None:
-        workspace = torch.empty(max(spec_prefix_attention_workspace_bytes(R, G, Hq, desc.heads, D, pages * desc.page_size), 1),
+        workspace = torch.empty(max(spec_prefix_attention_workspace_bytes(R, G, Hq, desc.heads, D, pages * desc.page_size, S), 1),
                                 dtype=torch.uint8, device=dev)
     _workspace(workspace)
     _same_device(q=q, cache=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale, page_table=page_table,

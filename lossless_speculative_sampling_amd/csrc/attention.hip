@@ -1,105 +1,663 @@
 // Attention of rows that share a long prefix of the paged cache.
 //
-// One wave per (row, query head): the wave walks the row's tokens with a running maximum and sum,
-// its lanes spread over the head's elements.  Right for every case, and slow: every row reads the
-// prefix again.
+// out = sum_t softmax_t(scale q . k_t) v_t over a prefix that all rows of a group see and a list
+// of slots of each row's own.  Two launches:
+//
+// 1. pieces.  The queries of a group that use one cache head (row by row, the heads of a row
+//    together) form tiles; a piece is a tile against a stretch of the prefix.  Every key and value
+//    of the stretch goes through LDS once for the whole tile.  The stretch's length is the same
+//    for all groups and chosen on the device from their lengths, so that the pieces of a ragged
+//    batch are alike and about as many as the card holds at once.  Further workgroups of the same
+//    launch take the suffix lists, one wave per row and cache head.
+// 2. join.  A row's pieces and its suffix are joined by their maxima and sums.
+//
+// Within a piece the scores are taken transposed, S^T = K Q^T: a lane then holds scores of one
+// query (its column), so the running maximum and sum need no exchange between lanes, and the
+// weights lie as the second product O^T = V^T P^T wants its right operand, so they go from one
+// matrix instruction to the next within the lane's registers.  (The order of the 32 keys inside
+// that product is free as long as both operands agree; it is the order the first product leaves.)
+// V^T comes out of LDS by the transposing read.
+//
+// The reference exponent of a query is moved only when a score exceeds it by more than 2^8:
+// weights stay below 2^8, where nothing is lost in fp32 sums nor, relatively, in the 16 bits of
+// the second product's operand, and nearly every step needs neither the exchange between lanes
+// nor the scaling of the output.
 #include "attention.h"
 
 namespace sv {
 namespace attn {
 
-template <typename C>
-__device__ __forceinline__ float cached(const void* p, int64_t i) {
-    return (float)static_cast<const C*>(p)[i];
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
+constexpr float kNone = -3.0e38f;  // reference exponent before any score
+constexpr float kSlack = 8.0f;     // scores up to 2^8 over the reference leave it where it is
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// ------------------------------------------------------------------------------------------
+// Matrix instructions and element types
+// ------------------------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ f32x4 mma(s16x8 a, s16x8 b, f32x4 c);
+template <>
+__device__ __forceinline__ f32x4 mma<__bf16>(s16x8 a, s16x8 b, f32x4 c) {
+    typedef __bf16 v __attribute__((ext_vector_type(8)));
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v, a), __builtin_bit_cast(v, b), c, 0, 0, 0);
 }
 template <>
-__device__ __forceinline__ float cached<uint8_t>(const void* p, int64_t i) {
-    return __builtin_amdgcn_cvt_f32_fp8((int)static_cast<const uint8_t*>(p)[i], 0);
+__device__ __forceinline__ f32x4 mma<_Float16>(s16x8 a, s16x8 b, f32x4 c) {
+    typedef _Float16 v __attribute__((ext_vector_type(8)));
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v, a), __builtin_bit_cast(v, b), c, 0, 0, 0);
 }
 
-// The group of row r: the largest g with row_start[g] <= r, or -1 outside every group.
-__device__ __forceinline__ int group_of(const Args& a, int r) {
-    int lo = -1, hi = a.G;  // row_start[lo] <= r < row_start[hi], with fences at either end
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.row_start[mid] <= r) lo = mid;
-        else hi = mid;
-    }
-    return lo >= 0 && r < a.row_start[lo + 1] ? lo : -1;
-}
-
-template <typename T, typename C>
-__global__ __launch_bounds__(kWave) void attention_kernel(Args a) {
-    constexpr int kPer = kMaxD / kWave;
-    const int r = blockIdx.x, h = blockIdx.y, lane = threadIdx.x;
-    const int g = group_of(a, r);
-    if (g < 0) return;
-    const int kvh = h / a.per;
-    const int page = a.cache.page_size;
-    float q[kPer], o[kPer];
+template <typename T>
+__device__ __forceinline__ s16x8 narrow8(const float (&x)[8]) {
+    typedef T v __attribute__((ext_vector_type(8)));
+    v r;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        const int d = lane + e * kWave;
-        q[e] = d < a.D ? (float)static_cast<const T*>(a.q)[r * a.q_row + h * a.q_head + d] : 0.0f;
-        o[e] = 0.0f;
+    for (int e = 0; e < 8; ++e) r[e] = (T)x[e];
+    return __builtin_bit_cast(s16x8, r);
+}
+
+// Eight cache elements as loaded, and as the matrix instructions take them.  An 8-bit float is
+// exact in either 16-bit type; its scale enters the scores' factor and the output.
+template <typename T, typename C>
+struct Raw;
+template <typename T>
+struct Raw<T, T> {
+    typedef u32x4 type;
+    static __device__ __forceinline__ s16x8 widen(u32x4 x) { return __builtin_bit_cast(s16x8, x); }
+};
+template <typename T>
+struct Raw<T, uint8_t> {
+    typedef u32x2 type;
+    static __device__ __forceinline__ s16x8 widen(u32x2 x) {
+        float f[8];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[w], false);
+            const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[w], true);
+            f[4 * w] = lo[0];
+            f[4 * w + 1] = lo[1];
+            f[4 * w + 2] = hi[0];
+            f[4 * w + 3] = hi[1];
+        }
+        return narrow8<T>(f);
     }
-    const float ks = a.cache.k_scale ? a.cache.k_scale[kvh] : 1.0f, vs = a.cache.v_scale ? a.cache.v_scale[kvh] : 1.0f;
-    const int64_t slots = (int64_t)a.cache.num_pages * page;
-    const int64_t most = (int64_t)a.max_pages * page;
-    int64_t L = a.max_pages ? a.prefix_len[g] : 0;
-    L = L < 0 ? 0 : (L > most ? most : L);
-    int S = a.max_suffix ? a.suffix_len[r] : 0;
+};
+
+// max over the four lanes that hold one query's scores (lanes l, l ^ 16, l ^ 32, l ^ 48)
+__device__ __forceinline__ float max_over_quarters(float x) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float sum_over_quarters(float x) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// ------------------------------------------------------------------------------------------
+// LDS tiles: rows of DP elements, 16-byte chunks exchanged within a row so that the lanes of one
+// read fall on different banks: keys are read 8 rows at a time at one chunk, values 4 rows at a
+// time at one pair of chunks.
+// ------------------------------------------------------------------------------------------
+template <int DP>
+__device__ __forceinline__ int k_at(int key, int chunk) {
+    return key * DP * 2 + ((chunk ^ (key & 7)) << 4);
+}
+template <int DP>
+__device__ __forceinline__ int v_at(int key, int chunk) {
+    return key * DP * 2 + ((chunk ^ ((key & 3) << 1)) << 4);
+}
+
+__device__ __forceinline__ s16x4 transposed4(const char* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+}
+
+// The running softmax of a wave's query blocks: lane l holds query l % 16 of each block, of the
+// output the elements 16 b + 4 (l / 16) .. + 3 of every block b, of the sum its own keys' part.
+template <int MB, int DP>
+struct State {
+    f32x4 o[MB][DP / 16];
+    float m[MB], l[MB];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+            m[i] = kNone;
+            l[i] = 0.0f;
+#pragma unroll
+            for (int b = 0; b < DP / 16; ++b) o[i][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+    }
+};
+
+// Scores of 32 keys (s[i][0]: keys 0..15, s[i][1]: 16..31; lane l has keys 4 (l / 16) .. + 3 of each)
+// into weights, and the product with their values from `vl`.  `valid`: which keys exist.
+template <typename T, int NB, int MB, int DP>
+__device__ __forceinline__ void weigh(State<MB, DP>& st, f32x4 (&s)[NB][2], uint32_t valid, float c, const char* vl) {
+    const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, i = lane & 15;
+    if (valid != 0xffffffffu) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!((valid >> (kb * 16 + g * 4 + e)) & 1)) s[n][kb][e] = -__builtin_inff();
+    }
+    s16x8 p[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        float top = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
+                          fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
+        if (__any(top * c > st.m[n] + kSlack)) {
+            const float m = fmaxf(st.m[n], max_over_quarters(top) * c);
+            const float f = exp2_fast(st.m[n] - m);
+            st.m[n] = m;
+            st.l[n] *= f;
+#pragma unroll
+            for (int b = 0; b < DP / 16; ++b) st.o[n][b] *= f;
+        }
+        float w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = exp2_fast(fmaf(s[n][e >> 2][e & 3], c, -st.m[n]));
+        st.l[n] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+        p[n] = narrow8<T>(w);
+    }
+    // lane i of a quarter reads row 4 g + i / 4 at elements 4 (i % 4) .. + 3 of the block and gets
+    // column i of the four rows
+#pragma unroll
+    for (int b = 0; b < DP / 16; ++b) {
+        const char* at = vl + v_at<DP>(g * 4 + (i >> 2), b * 2 + ((i & 3) >> 1)) + (i & 1) * 8;
+        const s16x4 lo = transposed4(at), hi = transposed4(at + 16 * DP * 2);
+        const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) st.o[n][b] = mma<T>(v, p[n], st.o[n][b]);
+    }
+}
+
+// A cache slot's offset in elements, or -1 where there is no token.
+__device__ __forceinline__ int64_t slot_offset(const Args& a, int64_t page, int in_page) {
+    return page >= 0 && page < a.cache.num_pages ? page * a.cache.page_stride + in_page * a.cache.token_stride : -1;
+}
+__device__ __forceinline__ int64_t slot_offset(const Args& a, int slot) {
+    const int page = slot >= 0 ? (a.page_shift >= 0 ? slot >> a.page_shift : slot / a.cache.page_size) : -1;
+    return slot_offset(a, page, slot - page * a.cache.page_size);
+}
+
+__device__ __forceinline__ int prefix_of(const Args& a, int g) {
+    const int64_t most = (int64_t)a.max_pages * a.cache.page_size;
+    const int64_t n = a.max_pages ? a.prefix_len[g] : 0;
+    return (int)(n < 0 ? 0 : (n > most ? most : n));
+}
+
+// Rows of group g within [0, R], first and number.
+__device__ __forceinline__ int2 rows_of(const Args& a, int g) {
+    int lo = a.row_start[g], hi = a.row_start[g + 1];
+    lo = lo < 0 ? 0 : (lo > a.R ? a.R : lo);
+    hi = hi > a.R ? a.R : hi;
+    return make_int2(lo, hi > lo ? hi - lo : 0);
+}
+
+// The factor of the scores in powers of two.  A negative one goes into the queries' signs, so that
+// the largest score stays the largest; zero is taken as next to nothing (masked scores are -inf).
+__device__ __forceinline__ float factor_of(const Args& a, int kvh, bool* negate) {
+    const float c = a.scale * (a.cache.k_scale ? a.cache.k_scale[kvh] : 1.0f) * kLog2e;
+    *negate = c < 0.0f;
+    return fmaxf(fabsf(c), 1e-37f);
+}
+
+// 16 queries as the right operand of the first product: lane l has query l % 16, elements
+// 32 kk + 8 (l / 16) .. + 7.
+template <typename T, int DP>
+__device__ __forceinline__ void load_queries(const Args& a, s16x8 (&q)[DP / 32], int row, int head, bool there, bool negate) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const T* p = static_cast<const T*>(a.q) + (int64_t)row * a.q_row + (int64_t)head * a.q_head;
+#pragma unroll
+    for (int kk = 0; kk < DP / 32; ++kk) {
+        const int d = kk * 32 + (lane >> 4) * 8;
+        s16x8 x = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (there && d < a.D) x = *reinterpret_cast<const s16x8*>(p + d);
+        if (negate) x ^= (short)0x8000;
+        q[kk] = x;
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// Pieces of the prefix
+// ------------------------------------------------------------------------------------------
+struct Piece {
+    int g, tile, begin, end;  // g < 0: none
+    int first, rows;          // the group's rows
+};
+
+struct PlanShared {
+    long long red64[kThreads / kWave];
+    int red[kThreads / kWave];
+    Piece piece;
+};
+
+// Piece number x of a cache head.  The stretch: the groups' tiles times lengths over the pieces
+// aimed at, less half a piece per tile for the stretches that end early.  The first workgroup
+// leaves every group's first piece and count for the join.
+template <int MT, int KT>
+__device__ __forceinline__ Piece find_piece(const Args& a, int x, bool leave, PlanShared& sh) {
+    long long work = 0, tiles = 0;
+    for (int g = threadIdx.x; g < a.G; g += kThreads) {
+        const int t = (rows_of(a, g).y * a.per + MT - 1) / MT;
+        work += (long long)t * prefix_of(a, g);
+        tiles += t;
+    }
+    work = block_sum(work, sh.red64);
+    tiles = block_sum(tiles, sh.red64);
+    long long parts = a.want - tiles / 2;
+    if (parts < a.want / 4) parts = a.want / 4;
+    if (parts < 1) parts = 1;
+    long long stretch = (work + parts - 1) / parts;
+    stretch = (stretch + KT - 1) / KT * KT;
+    if (stretch < KT) stretch = KT;
+    if (threadIdx.x == 0) sh.piece.g = -1;
+    int base = 0;
+    for (int g0 = 0; g0 < a.G; g0 += kThreads) {
+        const int g = g0 + threadIdx.x;
+        int t = 0, n = 0, len = 0;
+        int2 rows = make_int2(0, 0);
+        if (g < a.G) {
+            rows = rows_of(a, g);
+            len = prefix_of(a, g);
+            t = (rows.y * a.per + MT - 1) / MT;
+            n = t ? (int)((len + stretch - 1) / stretch) : 0;
+        }
+        int all;
+        const int at = base + block_exclusive_scan(t * n, sh.red, &all);
+        if (g < a.G && leave) a.groups[g] = make_int2(at, n);
+        if (x >= at && x < at + t * n) {
+            const int part = (x - at) / t;
+            sh.piece.g = g;
+            sh.piece.tile = (x - at) - part * t;
+            sh.piece.begin = (int)(part * stretch);
+            sh.piece.end = (int)(len < (part + 1) * stretch ? len : (part + 1) * stretch);
+            sh.piece.first = rows.x;
+            sh.piece.rows = rows.y;
+        }
+        base += all;
+    }
+    __syncthreads();
+    return sh.piece;
+}
+
+// Keys a workgroup takes per step: 32 per wave that stands alone over its keys, at least 64.
+constexpr int keys_of(int wq) { return wq == 1 ? 128 : 64; }
+
+template <typename T, typename C, int DP, int MB, int WQ>
+struct PieceLds {
+    static constexpr int KT = keys_of(WQ);
+    static constexpr int kTileBytes = KT * DP * 2;
+    static constexpr int kWK = 4 / WQ;
+    // the waves over the same queries meet in the same memory at the end
+    static constexpr int kMeet = (kWK - 1) * WQ * MB * (16 * DP * 4 + 16 * 4 * 2);
+    static constexpr int kBytes = 2 * kTileBytes > kMeet ? 2 * kTileBytes : kMeet;
+};
+
+template <typename T, typename C, int DP, int MB, int WQ>
+__device__ __forceinline__ void prefix_piece(const Args& a, int index, char* lds) {
+    typedef PieceLds<T, C, DP, MB, WQ> L;
+    constexpr int KT = L::KT, WK = L::kWK, MT = 16 * MB * WQ;
+    constexpr int kChunks = DP / 8;                    // 16-byte chunks of a row in LDS
+    constexpr int kLoads = KT * kChunks / kThreads;    // of K, and of V, per thread
+    constexpr int kStep = kThreads / kChunks;          // keys between a thread's loads
+    typedef typename Raw<T, C>::type raw;
+    __shared__ PlanShared plan;
+    __shared__ int64_t offs[2][KT];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
+    const int wq = wave % WQ, wk = wave / WQ;
+    const int kvh = index % a.heads;
+    const Piece pc = find_piece<MT, KT>(a, index / a.heads, index == 0, plan);
+    if (pc.g < 0) return;
+    const int M = pc.rows * a.per;
+    bool negate;
+    const float c = factor_of(a, kvh, &negate);
+
+    // the wave's query blocks, dealt out in turn so that a group that does not fill the tile still
+    // occupies all waves
+    s16x8 q[MB][DP / 32];
+    State<MB, DP> st;
+    st.clear();
+    int nb = 0;
+#pragma unroll
+    for (int n = 0; n < MB; ++n) {
+        const int base = pc.tile * MT + (n * WQ + wq) * 16, mq = base + (lane & 15);
+        if (base < M) nb = n + 1;
+        const bool there = mq < M;
+        const int row = there ? mq / a.per : 0, h = there ? mq - row * a.per : 0;
+        load_queries<T, DP>(a, q[n], pc.first + row, kvh * a.per + h, there, negate);
+    }
+
+    const C* kc = static_cast<const C*>(a.cache.k) + (int64_t)kvh * a.cache.head_stride;
+    const C* vc = static_cast<const C*>(a.cache.v) + (int64_t)kvh * a.cache.head_stride;
+    const int32_t* table = a.table + (int64_t)pc.g * a.max_pages;
+    const int chunk = tid % kChunks, key0 = tid / kChunks;
+    raw kr[kLoads], vr[kLoads];
+
+    // where the keys of the step at t lie, by the first KT threads
+    auto look_up = [&](int t, int buf) {
+        if (tid < KT) {
+            const int at = t + tid;
+            int64_t o = -1;
+            if (at < pc.end) {
+                const int page = a.page_shift >= 0 ? at >> a.page_shift : at / a.cache.page_size;
+                o = slot_offset(a, table[page], at - page * a.cache.page_size);
+            }
+            offs[buf][tid] = o;
+        }
+    };
+    auto load = [&](int buf) {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int64_t o = offs[buf][key0 + j * kStep];
+            raw x = {}, y = {};
+            if (o >= 0 && chunk * 8 < a.D) {
+                x = *reinterpret_cast<const raw*>(kc + o + chunk * 8);
+                y = *reinterpret_cast<const raw*>(vc + o + chunk * 8);
+            }
+            kr[j] = x;
+            vr[j] = y;
+        }
+    };
+    char* kl = lds;
+    char* vl = lds + L::kTileBytes;
+
+    look_up(pc.begin, 0);
+    __syncthreads();
+    load(0);
+    look_up(pc.begin + KT, 1);
+    int buf = 0;
+    for (int t = pc.begin; t < pc.end; t += KT, buf ^= 1) {
+        // which of the wave's keys exist (read before the offsets are overwritten)
+        uint32_t valid[KT / (32 * WK)];
+#pragma unroll
+        for (int sub = 0; sub < KT / (32 * WK); ++sub)
+            valid[sub] = (uint32_t)__ballot(offs[buf][(sub * WK + wk) * 32 + (lane & 31)] >= 0);
+        __syncthreads();  // the last step's tile has been read
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int key = key0 + j * kStep;
+            *reinterpret_cast<s16x8*>(kl + k_at<DP>(key, chunk)) = Raw<T, C>::widen(kr[j]);
+            *reinterpret_cast<s16x8*>(vl + v_at<DP>(key, chunk)) = Raw<T, C>::widen(vr[j]);
+        }
+        __syncthreads();
+        if (t + KT < pc.end) {
+            load(buf ^ 1);
+            look_up(t + 2 * KT, buf);
+        }
+        if (nb == 0) continue;
+#pragma unroll
+        for (int sub = 0; sub < KT / (32 * WK); ++sub) {
+            if (valid[sub] == 0) continue;
+            const int key = (sub * WK + wk) * 32;
+            f32x4 s[MB][2];
+#pragma unroll
+            for (int n = 0; n < MB; ++n) s[n][0] = s[n][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int kk = 0; kk < DP / 32; ++kk) {
+                    const s16x8 x = *reinterpret_cast<const s16x8*>(kl + k_at<DP>(key + kb * 16 + (lane & 15), kk * 4 + (lane >> 4)));
+#pragma unroll
+                    for (int n = 0; n < MB; ++n) s[n][kb] = mma<T>(x, q[n][kk], s[n][kb]);
+                }
+            weigh<T, MB, MB, DP>(st, s, valid[sub], c, vl + key * DP * 2);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < MB; ++n) st.l[n] = sum_over_quarters(st.l[n]);
+
+    // join the waves over different keys: all but the first leave theirs in LDS
+    if constexpr (WK > 1) {
+        __syncthreads();
+        float* mo = reinterpret_cast<float*>(lds);
+        float2* mm = reinterpret_cast<float2*>(lds + (WK - 1) * WQ * MB * 16 * DP * 4);
+        if (wk > 0) {
+#pragma unroll
+            for (int n = 0; n < MB; ++n) {
+                const int at = ((wk - 1) * WQ + wq) * MB + n;
+                if (lane < 16) mm[at * 16 + lane] = make_float2(st.m[n], st.l[n]);
+#pragma unroll
+                for (int b = 0; b < DP / 16; ++b)
+                    *reinterpret_cast<f32x4*>(mo + ((at * (DP / 16) + b) * 64 + lane) * 4) = st.o[n][b];
+            }
+        }
+        __syncthreads();
+        if (wk > 0) return;
+#pragma unroll
+        for (int n = 0; n < MB; ++n) {
+            float m = st.m[n];
+            float2 ml[WK - 1];
+#pragma unroll
+            for (int w = 0; w < WK - 1; ++w) {
+                ml[w] = mm[((w * WQ + wq) * MB + n) * 16 + (lane & 15)];
+                m = fmaxf(m, ml[w].x);
+            }
+            float f = exp2_fast(st.m[n] - m);
+            st.m[n] = m;
+            st.l[n] *= f;
+#pragma unroll
+            for (int b = 0; b < DP / 16; ++b) st.o[n][b] *= f;
+#pragma unroll
+            for (int w = 0; w < WK - 1; ++w) {
+                f = exp2_fast(ml[w].x - m);
+                st.l[n] += ml[w].y * f;
+#pragma unroll
+                for (int b = 0; b < DP / 16; ++b)
+                    st.o[n][b] += *reinterpret_cast<const f32x4*>(mo + (((((w * WQ + wq) * MB + n) * (DP / 16)) + b) * 64 + lane) * 4) * f;
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < MB; ++n) {
+        const int in_tile = (n * WQ + wq) * 16 + (lane & 15);
+        if (pc.tile * MT + in_tile >= M) continue;
+        const int64_t at = (int64_t)index * MT + in_tile;
+        if (lane < 16) a.piece_ml[at] = make_float2(st.m[n], st.l[n]);
+#pragma unroll
+        for (int b = 0; b < DP / 16; ++b) {
+            const int d = b * 16 + (lane >> 4) * 4;
+            if (d < a.D) *reinterpret_cast<f32x4*>(a.piece_o + at * a.D + d) = st.o[n][b];
+        }
+    }
+}
+
+// The group of row r, or -1: how many groups begin at or before it, counted by `width` lanes that
+// share the row (a power of two; `lane` < width).
+__device__ __forceinline__ int group_of(const Args& a, int r, int lane, int width) {
+    int n = 0;
+    for (int g0 = 0; g0 < a.G; g0 += width) {
+        const int g = g0 + lane;
+        int mine = g < a.G && a.row_start[g] <= r ? 1 : 0;
+        for (int s = 1; s < width; s <<= 1) mine += __shfl_xor(mine, s);
+        n += mine;
+        if (mine < width) break;
+    }
+    const int g = n - 1;
+    return g >= 0 && r < a.row_start[g + 1] ? g : -1;
+}
+
+// ------------------------------------------------------------------------------------------
+// The suffix lists: one wave per (row, cache head, block of 16 of its query heads), 32 slots at a
+// time.  Keys go from memory into the first product's operand as they lie; values through the
+// wave's own part of LDS.
+// ------------------------------------------------------------------------------------------
+template <typename T, typename C, int DP>
+__device__ __forceinline__ void suffix_wave(const Args& a, int64_t task, char* lds) {
+    typedef typename Raw<T, C>::type raw;
+    const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, i = lane & 15;
+    const int blocks = (a.per + 15) / 16;
+    if (task >= (int64_t)a.R * a.heads * blocks) return;
+    const int block = (int)(task % blocks), kvh = (int)(task / blocks % a.heads), r = (int)(task / blocks / a.heads);
+    if (group_of(a, r, lane, kWave) < 0) return;
+    int S = a.suffix_len[r];
     S = S < 0 ? 0 : (S > a.max_suffix ? a.max_suffix : S);
-    float m = -__builtin_inff(), l = 0.0f;
-    for (int64_t t = 0; t < L + S; ++t) {
-        int64_t slot;
-        if (t < L) {
-            const int64_t id = a.table[(int64_t)g * a.max_pages + t / page];
-            slot = id >= 0 && id < a.cache.num_pages ? id * page + t % page : -1;
-        } else {
-            slot = a.lists[(int64_t)r * a.max_suffix + (t - L)];
-        }
-        if (slot < 0 || slot >= slots) continue;
-        const int64_t at = slot / page * a.cache.page_stride + slot % page * a.cache.token_stride + (int64_t)kvh * a.cache.head_stride;
-        float s = 0.0f;
+    const int32_t* list = a.lists + (int64_t)r * a.max_suffix;
+    bool negate;
+    const float c = factor_of(a, kvh, &negate);
+    s16x8 q[1][DP / 32];
+    const int h = block * 16 + i;
+    load_queries<T, DP>(a, q[0], r, kvh * a.per + h, h < a.per, negate);
+    const C* kc = static_cast<const C*>(a.cache.k) + (int64_t)kvh * a.cache.head_stride;
+    const C* vc = static_cast<const C*>(a.cache.v) + (int64_t)kvh * a.cache.head_stride;
+    State<1, DP> st;
+    st.clear();
+    for (int t = 0; t < S; t += 32) {
+        raw x[2][DP / 32], y[2][DP / 32];
+        uint32_t valid = 0;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const int d = lane + e * kWave;
-            if (d < a.D) s += q[e] * cached<C>(a.cache.k, at + d);
+        for (int kb = 0; kb < 2; ++kb) {
+            const int at = t + kb * 16 + i;
+            const int64_t o = at < S ? slot_offset(a, list[at]) : -1;
+            valid |= ((uint32_t)__ballot(o >= 0) & 0xffffu) << (kb * 16);
+#pragma unroll
+            for (int kk = 0; kk < DP / 32; ++kk) {
+                const int d = kk * 32 + g * 8;
+                x[kb][kk] = raw{};
+                y[kb][kk] = raw{};
+                if (o >= 0 && d < a.D) {
+                    x[kb][kk] = *reinterpret_cast<const raw*>(kc + o + d);
+                    y[kb][kk] = *reinterpret_cast<const raw*>(vc + o + d);
+                }
+            }
         }
-        s = wave_sum(s) * ks * a.scale;
-        if (s == -__builtin_inff()) continue;
-        const float top = s > m ? s : (s == s ? m : s);
-        const float keep = m == -__builtin_inff() ? 0.0f : expf(m - top), w = expf(s - top);
-        l = l * keep + w;
+        if (valid == 0) continue;
+        f32x4 s[1][2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            s[0][kb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int kk = 0; kk < DP / 32; ++kk) {
+                s[0][kb] = mma<T>(Raw<T, C>::widen(x[kb][kk]), q[0][kk], s[0][kb]);
+                *reinterpret_cast<s16x8*>(lds + v_at<DP>(kb * 16 + i, kk * 4 + g)) = Raw<T, C>::widen(y[kb][kk]);
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+        weigh<T, 1, 1, DP>(st, s, valid, c, lds);
+        __builtin_amdgcn_wave_barrier();
+    }
+    st.l[0] = sum_over_quarters(st.l[0]);
+    if (h >= a.per) return;
+    const int64_t at = (int64_t)r * a.q_heads + kvh * a.per + h;
+    if (g == 0) a.suffix_ml[at] = make_float2(st.m[0], st.l[0]);
+#pragma unroll
+    for (int b = 0; b < DP / 16; ++b) {
+        const int d = b * 16 + g * 4;
+        if (d < a.D) *reinterpret_cast<f32x4*>(a.suffix_o + at * a.D + d) = st.o[0][b];
+    }
+}
+
+template <typename T, typename C, int DP, int MB, int WQ>
+__global__ __launch_bounds__(kThreads) void attention_pieces_kernel(Args a) {
+    constexpr int kSuffixBytes = 4 * 32 * DP * 2;
+    constexpr int kPieceBytes = PieceLds<T, C, DP, MB, WQ>::kBytes;
+    __shared__ __align__(16) char lds[kPieceBytes > kSuffixBytes ? kPieceBytes : kSuffixBytes];
+    const int pieces = a.slots * a.heads;
+    if ((int)blockIdx.x < pieces) {
+        prefix_piece<T, C, DP, MB, WQ>(a, blockIdx.x, lds);
+    } else {
+        const int wave = threadIdx.x >> 6;
+        suffix_wave<T, C, DP>(a, (int64_t)(blockIdx.x - pieces) * 4 + wave, lds + wave * 32 * DP * 2);
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// The join: DP / 4 lanes per (row, query head), four elements each.
+// ------------------------------------------------------------------------------------------
+template <typename T, int DP>
+__global__ __launch_bounds__(kThreads) void attention_join_kernel(Args a, int mt) {
+    constexpr int kLanes = DP / 4;
+    const int lane = threadIdx.x % kLanes;
+    const int64_t pair = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+    if (pair >= (int64_t)a.R * a.q_heads) return;
+    const int r = (int)(pair / a.q_heads), h = (int)(pair % a.q_heads), kvh = h / a.per;
+    const int g = group_of(a, r, lane, kLanes);
+    if (g < 0) return;
+    const int d = lane * 4;
+    float m = kNone, l = 0.0f;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto add = [&](float2 ml, const float* from) {
+        const float top = fmaxf(m, ml.x);
+        const float keep = exp2_fast(m - top), f = exp2_fast(ml.x - top);
         m = top;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const int d = lane + e * kWave;
-            o[e] = o[e] * keep + (d < a.D ? w * cached<C>(a.cache.v, at + d) : 0.0f);
+        l = l * keep + ml.y * f;
+        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (d < a.D) x = *reinterpret_cast<const f32x4*>(from + d);
+        o = o * keep + x * f;
+    };
+    if (a.max_suffix) add(a.suffix_ml[pair], a.suffix_o + pair * a.D);
+    if (a.slots) {
+        const int2 rows = rows_of(a, g), span = a.groups[g];
+        const int q = (r - rows.x) * a.per + h - kvh * a.per;
+        const int tiles = (rows.y * a.per + mt - 1) / mt, tile = q / mt;
+        for (int s = 0; s < span.y; ++s) {
+            const int64_t at = ((int64_t)(span.x + s * tiles + tile) * a.heads + kvh) * mt + (q - tile * mt);
+            add(a.piece_ml[at], a.piece_o + at * a.D);
         }
     }
+    if (d < a.D) {
+        const float f = l == 0.0f ? 0.0f : (a.cache.v_scale ? a.cache.v_scale[kvh] : 1.0f) / l;
+        typedef T v4 __attribute__((ext_vector_type(4)));
+        v4 y;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        const int d = lane + e * kWave;
-        if (d < a.D) static_cast<T*>(a.out)[r * a.out_row + h * a.out_head + d] = (T)(l == 0.0f ? 0.0f : o[e] * vs / l);
+        for (int e = 0; e < 4; ++e) y[e] = (T)(l == 0.0f ? 0.0f : o[e] * f);
+        *reinterpret_cast<v4*>(static_cast<T*>(a.out) + (int64_t)r * a.out_row + (int64_t)h * a.out_head + d) = y;
     }
-    if (a.lse && lane == 0) a.lse[(int64_t)r * a.q_heads + h] = l == 0.0f ? -__builtin_inff() : m + logf(l);
+    if (a.lse && lane == 0) a.lse[pair] = l == 0.0f ? -__builtin_inff() : (m + log2f(l)) * kLn2;
+}
+
+template <typename T, typename C, int DP, int MB, int WQ>
+static void launch_tile(const Args& a, hipStream_t stream) {
+    const unsigned blocks = (unsigned)(a.slots * a.heads + a.suffix_blocks);
+    if (blocks)
+        hipLaunchKernelGGL((attention_pieces_kernel<T, C, DP, MB, WQ>), dim3(blocks), dim3(kThreads), 0, stream, a);
+    const int64_t per = kThreads / (DP / 4), pairs = (int64_t)a.R * a.q_heads;
+    hipLaunchKernelGGL((attention_join_kernel<T, DP>), dim3((unsigned)((pairs + per - 1) / per)), dim3(kThreads), 0, stream, a,
+                       16 * MB * WQ);
 }
 
 template <typename T, typename C>
-static void launch_typed(const Args& a, hipStream_t stream) {
-    hipLaunchKernelGGL((attention_kernel<T, C>), dim3((unsigned)a.R, (unsigned)a.q_heads), dim3(kWave), 0, stream, a);
+static void launch_typed(const Args& a, const Tile& t, hipStream_t stream) {
+    if (a.D > 128) {
+        if (t.mb == 1) launch_tile<T, C, 256, 1, 2>(a, stream);
+        else if (t.wq == 2) launch_tile<T, C, 256, 2, 2>(a, stream);
+        else launch_tile<T, C, 256, 2, 4>(a, stream);
+    } else if (a.D > 64) {
+        if (t.mb == 1) launch_tile<T, C, 128, 1, 1>(a, stream);
+        else if (t.wq == 1) launch_tile<T, C, 128, 2, 1>(a, stream);
+        else if (t.wq == 2) launch_tile<T, C, 128, 2, 2>(a, stream);
+        else launch_tile<T, C, 128, 2, 4>(a, stream);
+    } else {
+        if (t.mb == 1) launch_tile<T, C, 64, 1, 1>(a, stream);
+        else if (t.wq == 1) launch_tile<T, C, 64, 2, 1>(a, stream);
+        else if (t.wq == 2) launch_tile<T, C, 64, 2, 2>(a, stream);
+        else launch_tile<T, C, 64, 2, 4>(a, stream);
+    }
 }
 
-void launch(const Args& a, int dtype, hipStream_t stream) {
+void launch(const Args& a, const Tile& t, int dtype, hipStream_t stream) {
     const bool eight = a.cache.dtype == SPEC_E4M3;
     if (dtype == SPEC_BF16) {
-        if (eight) launch_typed<__bf16, uint8_t>(a, stream);
-        else launch_typed<__bf16, __bf16>(a, stream);
+        if (eight) launch_typed<__bf16, uint8_t>(a, t, stream);
+        else launch_typed<__bf16, __bf16>(a, t, stream);
     } else {
-        if (eight) launch_typed<_Float16, uint8_t>(a, stream);
-        else launch_typed<_Float16, _Float16>(a, stream);
+        if (eight) launch_typed<_Float16, uint8_t>(a, t, stream);
+        else launch_typed<_Float16, _Float16>(a, t, stream);
     }
 }
 

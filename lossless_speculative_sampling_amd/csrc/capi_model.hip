@@ -176,10 +176,15 @@ int spec_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
     return launched();
 }
 
-size_t spec_prefix_attention_workspace_bytes(int R, int G, int q_heads, int heads, int head_dim, int64_t max_prefix) {
+size_t spec_prefix_attention_workspace_bytes(int R, int G, int q_heads, int heads, int head_dim, int64_t max_prefix,
+                                             int max_suffix) {
     if (R < 0 || G < 1 || heads < 1 || q_heads < heads || q_heads % heads != 0 || q_heads > (1 << 16)) return 0;
-    if (head_dim < 8 || head_dim > attn::kMaxD || head_dim % 8 != 0 || max_prefix < 0 || max_prefix > 0x7fffffffll) return 0;
-    return 256;
+    if (head_dim < 8 || head_dim > attn::kMaxD || head_dim % 8 != 0 || max_prefix < 0 || max_prefix > 0x7fffffffll ||
+        max_suffix < 0 || G > kMaxGroups || (int64_t)R * q_heads > 8 * kMaxGroups)
+        return 0;
+    const attn::Plan p = attn::plan_of(R, G, q_heads, heads, head_dim, max_prefix, max_suffix);
+    if ((int64_t)p.slots * heads + p.suffix_blocks > kMaxGroups) return 0;
+    return p.bytes;
 }
 
 int spec_prefix_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride, int dtype, int R, int q_heads,
@@ -197,7 +202,8 @@ int spec_prefix_attention(const void* q, int64_t q_row_stride, int64_t q_head_st
     const int rc = check_cache(cache, dtype);
     if (rc != SPEC_OK) return rc;
     const int64_t most = (int64_t)max_pages * cache->page_size;
-    const size_t need = spec_prefix_attention_workspace_bytes(R, G, q_heads, cache->heads, cache->head_dim, most);
+    const size_t need = spec_prefix_attention_workspace_bytes(R, G, q_heads, cache->heads, cache->head_dim, most,
+                                                             max_suffix);
     if (need == 0) return SPEC_EINVAL;
     const uintptr_t kv_align = cache->dtype == SPEC_E4M3 ? 8 : 16;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(cache->k, kv_align) || !aligned(cache->v, kv_align) ||
@@ -229,7 +235,19 @@ int spec_prefix_attention(const void* q, int64_t q_row_stride, int64_t q_head_st
     a.out_row = out_row_stride;
     a.out_head = out_head_stride;
     a.lse = out_lse;
-    attn::launch(a, dtype, stream);
+    const int page = cache->page_size;
+    a.page_shift = (page & (page - 1)) == 0 ? __builtin_ctz((unsigned)page) : -1;
+    const attn::Plan p = attn::plan_of(R, G, q_heads, cache->heads, cache->head_dim, most, max_suffix);
+    char* ws = static_cast<char*>(workspace);
+    a.want = p.want;
+    a.slots = p.slots;
+    a.suffix_blocks = (int)p.suffix_blocks;
+    a.piece_o = reinterpret_cast<float*>(ws + p.piece_o);
+    a.piece_ml = reinterpret_cast<float2*>(ws + p.piece_ml);
+    a.suffix_o = reinterpret_cast<float*>(ws + p.suffix_o);
+    a.suffix_ml = reinterpret_cast<float2*>(ws + p.suffix_ml);
+    a.groups = reinterpret_cast<int2*>(ws + p.groups);
+    attn::launch(a, p.tile, dtype, stream);
     return launched();
 }
 

@@ -101,9 +101,10 @@ def test_attention_cache_errors(bad, rc):
 
 def test_attention_workspace():
     f = capi.spec_prefix_attention_workspace_bytes
-    assert f(8, 2, 8, 2, 128, 4096) > 0 and f(0, 1, 8, 8, 8, 0) > 0
-    for bad in ((-1, 1, 8, 8, 64, 10), (4, 0, 8, 8, 64, 10), (4, 1, 8, 3, 64, 10), (4, 1, 8, 0, 64, 10), (4, 1, 8, 8, 257, 10),
-                (4, 1, 8, 8, 12, 10), (4, 1, 8, 8, 64, -1), (4, 1, 8, 8, 64, 1 << 31)):
+    assert f(8, 2, 8, 2, 128, 4096, 5) > f(8, 2, 8, 2, 128, 4096, 0) > 0 and f(0, 1, 8, 8, 8, 0, 0) > 0
+    for bad in ((-1, 1, 8, 8, 64, 10, 0), (4, 0, 8, 8, 64, 10, 0), (4, 1, 8, 3, 64, 10, 0), (4, 1, 8, 0, 64, 10, 0),
+                (4, 1, 8, 8, 257, 10, 0), (4, 1, 8, 8, 12, 10, 0), (4, 1, 8, 8, 64, -1, 0), (4, 1, 8, 8, 64, 1 << 31, 0),
+                (4, 1, 8, 8, 64, 10, -1), (1 << 30, 1, 8, 8, 64, 10, 0), (4, 1 << 30, 8, 8, 64, 10, 0)):
         assert f(*bad) == 0
 
 
