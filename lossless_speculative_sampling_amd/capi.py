@@ -7,6 +7,7 @@ or unloadable library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -508,41 +509,46 @@ def pyramid_verify(draft: Optional[torch.Tensor], verifier: torch.Tensor, K: int
 
 # ---- the steps on either side of the verification.  These take strided tensors where the C ABI has
 # strides, and run on the device of their tensors (its current stream unless `stream` is given),
-# whichever device is current. ----
+# whichever device is current.  A call here is a few microseconds of GPU work at its smallest, so the
+# checks are written to cost little: one comparison each, messages made only when one fails. ----
 _HALF = {torch.bfloat16: SPEC_BF16, torch.float16: SPEC_FP16}
 _PROBS = {torch.float32: SPEC_FP32, **_HALF}
+_I32, _F32, _F64, _U8 = torch.int32, torch.float32, torch.float64, torch.uint8
 
 
-def _same_device(**tensors) -> torch.device:
-    """The one GPU that every given tensor lies on."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        _need(t.is_cuda, f"{name}: device tensor expected")
-        dev = t.device if dev is None else dev
-        _need(t.device == dev, f"{name} lies on {t.device}, the others on {dev}")
-    return dev
+def _on_one_device(dev: int, tensors):
+    """Raises unless every given tensor lies on GPU `dev`."""
+    if dev < 0:
+        raise ValueError("device tensor expected")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("device tensor expected" if t.get_device() < 0 else
+                             f"tensors lie on different devices: cuda:{dev} and cuda:{t.get_device()}")
 
 
 def _whole(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple):
-    _need(t is not None, f"{name} is required")
-    _need(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
-    _need(t.shape == torch.Size(shape), f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    _need(t.is_contiguous(), f"{name} must be contiguous")
+    if t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _need(t is not None, f"{name} is required")
+        _need(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
+        _need(tuple(t.shape) == shape, f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _inner(name: str, t: torch.Tensor):
-    _need(t.stride(-1) == 1 or t.shape[-1] == 1, f"{name}: the last dimension must be contiguous")
+def _strides(name: str, t: torch.Tensor) -> tuple:
+    """The outer strides of a tensor whose last dimension is contiguous."""
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return st
 
 
-def _call(fn: str, dev: torch.device, stream, *args):
-    """Calls the library with the stream last, on `dev`."""
-    if dev.index == torch.cuda.current_device():
-        rc = getattr(load().cdll, fn)(*args, _stream(stream))
-    else:
+def _call(fn: str, dev: int, stream, *args):
+    """Calls the library with the stream last, on GPU `dev`."""
+    here = torch._C._cuda_getDevice()
+    if dev != here:
         with torch.cuda.device(dev):
-            rc = getattr(load().cdll, fn)(*args, _stream(stream))
+            return _call(fn, dev, stream, *args)
+    rc = getattr(load().cdll, fn)(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if rc != SPEC_OK:
         raise SpecError(fn, rc)
 
@@ -560,6 +566,7 @@ class ProbsOut:
     status: torch.Tensor      # [B] int32 status bits
 
 
+@functools.lru_cache(maxsize=1024)
 def spec_verify_probs_workspace_bytes(B: int, V: int) -> int:
     return int(load().cdll.spec_verify_probs_workspace_bytes(B, V))
 
@@ -570,43 +577,49 @@ def spec_verify_probs(draft: Optional[torch.Tensor], target: torch.Tensor, token
     """Verification from given probabilities, draft [B][K][V] (None with SPEC_UNIFORM_DRAFT or
     SPEC_POINT_DRAFT) and target [B][K+1][V] in fp32, bf16 or fp16, and given random numbers accept_u
     [B][K] and sample_v [B] in fp32 or fp64; tokens [B][K] and draft_lens [B] int32."""
-    _need(target.dim() == 3 and target.dtype in _PROBS, "target must be [B][K+1][V] in fp32, bf16 or fp16")
+    code = _PROBS.get(target.dtype)
+    if target.dim() != 3 or code is None:
+        raise ValueError("target must be [B][K+1][V] in fp32, bf16 or fp16")
     B, rows, V = target.shape
     K = rows - 1
-    _need(B >= 1 and K >= 1 and V >= 1, f"target {tuple(target.shape)} holds no drafted position")
-    _inner("target", target)
-    if draft is None:
-        _need(flags != 0, "draft probabilities are required without SPEC_UNIFORM_DRAFT or SPEC_POINT_DRAFT")
-        ds = (0, 0)
-    else:
-        _need(draft.dtype == target.dtype, "draft and target must have the same dtype")
-        _need(draft.shape == (B, K, V), f"draft must be {(B, K, V)}, got {tuple(draft.shape)}")
-        _inner("draft", draft)
-        ds = (draft.stride(0), draft.stride(1))
-    _whole("tokens", tokens, torch.int32, (B, K))
-    _need(accept_u.dtype in (torch.float32, torch.float64), "accept_u must be float32 or float64")
-    _whole("accept_u", accept_u, accept_u.dtype, (B, K))
-    _whole("sample_v", sample_v, accept_u.dtype, (B,))
+    if B < 1 or K < 1 or V < 1:
+        raise ValueError(f"target {tuple(target.shape)} holds no drafted position")
+    ts = _strides("target", target)
+    ds = (0, 0)
+    if draft is not None:
+        if draft.dtype is not target.dtype or draft.shape != (B, K, V):
+            _need(draft.dtype == target.dtype, "draft and target must have the same dtype")
+            raise ValueError(f"draft must be {(B, K, V)}, got {tuple(draft.shape)}")
+        ds = _strides("draft", draft)
+    elif not flags:
+        raise ValueError("draft probabilities are required without SPEC_UNIFORM_DRAFT or SPEC_POINT_DRAFT")
+    _whole("tokens", tokens, _I32, (B, K))
+    ut = accept_u.dtype
+    if ut is not _F32 and ut is not _F64:
+        raise ValueError("accept_u must be float32 or float64")
+    _whole("accept_u", accept_u, ut, (B, K))
+    _whole("sample_v", sample_v, ut, (B,))
     if draft_lens is not None:
-        _whole("draft_lens", draft_lens, torch.int32, (B,))
-    dev = target.device
+        _whole("draft_lens", draft_lens, _I32, (B,))
+    dev = target.get_device()
     if out is None:
-        ints = torch.empty(B * (K + 5), dtype=torch.int32, device=dev)
-        out = ProbsOut(ints[:B], ints[B:2 * B], ints[4 * B:].view(B, K + 1), ints[3 * B:4 * B].view(torch.float32),
-                       ints[2 * B:3 * B])
+        k, tstar, status, mass = torch.empty((4, B), dtype=_I32, device=target.device).unbind()
+        out = ProbsOut(k, tstar, torch.empty((B, rows), dtype=_I32, device=target.device), mass.view(_F32), status)
     else:
-        for name, shape in (("k", (B,)), ("tstar", (B,)), ("emitted", (B, K + 1)), ("status", (B,))):
-            _whole(f"out.{name}", getattr(out, name), torch.int32, shape)
-        _whole("out.resid_mass", out.resid_mass, torch.float32, (B,))
+        for name in ("k", "tstar", "status"):
+            _whole(f"out.{name}", getattr(out, name), _I32, (B,))
+        _whole("out.emitted", out.emitted, _I32, (B, rows))
+        _whole("out.resid_mass", out.resid_mass, _F32, (B,))
     if workspace is None:
-        workspace = torch.empty(max(spec_verify_probs_workspace_bytes(B, V), 1), dtype=torch.uint8, device=dev)
-    _workspace(workspace)
-    _same_device(target=target, draft=draft, tokens=tokens, accept_u=accept_u, sample_v=sample_v, draft_lens=draft_lens,
-                 out=out.k, emitted=out.emitted, workspace=workspace)
-    _call("spec_verify_probs", dev, stream, _data(draft), *ds, _data(target), target.stride(0), target.stride(1),
-          _PROBS[target.dtype], B, K, V, _data(tokens), _data(draft_lens), _data(accept_u), _data(sample_v),
-          SPEC_FP64 if accept_u.dtype == torch.float64 else SPEC_FP32, flags, _data(out.k), _data(out.tstar),
-          _data(out.emitted), _data(out.resid_mass), _data(out.status), _data(workspace), workspace.numel())
+        workspace = torch.empty(spec_verify_probs_workspace_bytes(B, V), dtype=_U8, device=target.device)
+    else:
+        _workspace(workspace)
+    _on_one_device(dev, (target, draft, tokens, accept_u, sample_v, draft_lens, out.k, out.tstar, out.emitted,
+                         out.resid_mass, out.status, workspace))
+    _call("spec_verify_probs", dev, stream, _data(draft), ds[0], ds[1], target.data_ptr(), ts[0], ts[1], code, B, K, V,
+          tokens.data_ptr(), _data(draft_lens), accept_u.data_ptr(), sample_v.data_ptr(),
+          SPEC_FP64 if ut is _F64 else SPEC_FP32, flags, out.k.data_ptr(), out.tstar.data_ptr(), out.emitted.data_ptr(),
+          out.resid_mass.data_ptr(), out.status.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -622,27 +635,27 @@ def spec_tree_rows(tokens: torch.Tensor, parents: torch.Tensor, slots: torch.Ten
                    max_depth: int, out: Optional[TreeRows] = None, stream=None) -> TreeRows:
     """The rows of draft trees [B][N] (parents first, as in mirror_tree_lookup) on contexts of ctx_len [B]
     tokens, node n of request b at cache slot slots[b][n]."""
-    _need(tokens.dim() == 2, "tokens must be [B][N]")
-    B, N = tokens.shape
-    _whole("tokens", tokens, torch.int32, (B, N))
-    _whole("parents", parents, torch.int32, (B, N))
-    _whole("slots", slots, torch.int32, (B, N))
-    _whole("ctx_len", ctx_len, torch.int32, (B,))
-    _need(max_depth >= 1, "max_depth must be at least 1")
-    dev = tokens.device
+    if tokens.dim() != 2:
+        raise ValueError("tokens must be [B][N]")
+    shape = B, N = tuple(tokens.shape)
+    _whole("tokens", tokens, _I32, shape)
+    _whole("parents", parents, _I32, shape)
+    _whole("slots", slots, _I32, shape)
+    _whole("ctx_len", ctx_len, _I32, (B,))
+    if max_depth < 1:
+        raise ValueError("max_depth must be at least 1")
     if out is None:
-        ints = torch.empty(B * N * (max_depth + 3), dtype=torch.int32, device=dev)
-        n = B * N
-        out = TreeRows(ints[:n].view(B, N), ints[n:2 * n].view(B, N), ints[3 * n:].view(B, N, max_depth),
-                       ints[2 * n:3 * n].view(B, N))
+        pos, app, length = torch.empty((3, B, N), dtype=_I32, device=tokens.device).unbind()
+        out = TreeRows(pos, app, torch.empty((B, N, max_depth), dtype=_I32, device=tokens.device), length)
     else:
         for name in ("positions", "append_slots", "suffix_len"):
-            _whole(f"out.{name}", getattr(out, name), torch.int32, (B, N))
-        _whole("out.suffix_slots", out.suffix_slots, torch.int32, (B, N, max_depth))
-    _same_device(tokens=tokens, parents=parents, slots=slots, ctx_len=ctx_len, out=out.suffix_slots,
-                 positions=out.positions)
-    _call("spec_tree_rows", dev, stream, _data(tokens), _data(parents), _data(slots), _data(ctx_len), B, N, max_depth,
-          _data(out.positions), _data(out.append_slots), _data(out.suffix_slots), _data(out.suffix_len))
+            _whole(f"out.{name}", getattr(out, name), _I32, shape)
+        _whole("out.suffix_slots", out.suffix_slots, _I32, (B, N, max_depth))
+    dev = tokens.get_device()
+    _on_one_device(dev, (tokens, parents, slots, ctx_len, out.positions, out.append_slots, out.suffix_slots, out.suffix_len))
+    _call("spec_tree_rows", dev, stream, tokens.data_ptr(), parents.data_ptr(), slots.data_ptr(), ctx_len.data_ptr(), B, N,
+          max_depth, out.positions.data_ptr(), out.append_slots.data_ptr(), out.suffix_slots.data_ptr(),
+          out.suffix_len.data_ptr())
     return out
 
 
@@ -673,21 +686,23 @@ class KVCache:
     v_scale: Optional[torch.Tensor] = None
 
     def described(self) -> _Cache:
-        k, v = self.k, self.v
-        _need(k.dim() == 4 and k.shape == v.shape, "cache: k and v must be [num_pages][page_size][heads][head_dim] alike")
-        _need(k.dtype == v.dtype, "cache: k and v must have the same dtype")
-        _need(k.stride() == v.stride(), "cache: k and v must have the same strides")
-        _need(k.stride(3) == 1 or k.shape[3] == 1, "cache: head_dim must be contiguous")
-        eight = k.dtype == torch.float8_e4m3fn
-        _need(eight or k.dtype in _HALF, f"cache: unsupported dtype {k.dtype}")
-        for name, x in (("k_scale", self.k_scale), ("v_scale", self.v_scale)):
-            if x is not None:
-                _need(eight, f"cache: {name} belongs to an 8-bit cache")
-                _whole(f"cache.{name}", x, torch.float32, (k.shape[2],))
-        pages, page, heads, dim = k.shape
-        ps, ts, hs, _ = k.stride()
-        return _Cache(k.data_ptr(), v.data_ptr(), SPEC_E4M3 if eight else _HALF[k.dtype], pages, page, heads, dim, ps, ts,
-                      hs, _data(self.k_scale), _data(self.v_scale))
+        k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
+        shape, st = k.shape, k.stride()
+        eight = k.dtype is torch.float8_e4m3fn
+        code = SPEC_E4M3 if eight else _HALF.get(k.dtype)
+        if len(shape) != 4 or v.shape != shape or v.dtype is not k.dtype or v.stride() != st or code is None:
+            _need(k.dim() == 4 and k.shape == v.shape, "cache: k and v must be [num_pages][page_size][heads][head_dim] alike")
+            _need(k.dtype == v.dtype, "cache: k and v must have the same dtype")
+            _need(code is not None, f"cache: unsupported dtype {k.dtype}")
+            raise ValueError("cache: k and v must have the same strides")
+        if st[3] != 1 and shape[3] > 1:
+            raise ValueError("cache: head_dim must be contiguous")
+        if ks is not None or vs is not None:
+            _need(eight, "cache: scales belong to an 8-bit cache")
+            for name, x in (("k_scale", ks), ("v_scale", vs)):
+                if x is not None:
+                    _whole(f"cache.{name}", x, _F32, (shape[2],))
+        return _Cache(k.data_ptr(), v.data_ptr(), code, *shape, *st[:3], _data(ks), _data(vs))
 
 
 def spec_kv_append(k: Optional[torch.Tensor], v: Optional[torch.Tensor], positions: Optional[torch.Tensor],
@@ -698,52 +713,61 @@ def spec_kv_append(k: Optional[torch.Tensor], v: Optional[torch.Tensor], positio
     rotates q [T][q_heads][head_dim] into q_out (allocated here unless given; q itself: in place), which is
     returned.  k, v, slots and cache may all be None (queries only), and q (keys and values only)."""
     lead = q if q is not None else k
-    _need(lead is not None and lead.dim() == 3, "q or k must be given, as [T][heads][head_dim]")
-    _need((k is None) == (v is None) == (cache is None) and (k is None or slots is not None),
-          "k, v, slots and cache come together")
+    if lead is None or lead.dim() != 3:
+        raise ValueError("q or k must be given, as [T][heads][head_dim]")
     T, _, D = lead.shape
-    _need(lead.dtype in _HALF, f"unsupported dtype {lead.dtype}")
-    desc, kst, heads = None, (0, 0, 0, 0), 0
-    if k is not None:
+    code = _HALF.get(lead.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {lead.dtype}")
+    desc, heads, q_heads, rot, rscale, rflags = None, 0, 0, 0, 1.0, 0
+    freqs = ks = vs = qs = os = None
+    if k is not None and v is not None and cache is not None and slots is not None:
+        if k.dim() != 3 or v.shape != k.shape or k.dtype is not lead.dtype or v.dtype is not lead.dtype:
+            _need(v.shape == k.shape, "k and v must have the same shape")
+            _need(k.dim() == 3, "k must be [T][heads][head_dim]")
+            raise ValueError("q, k and v must have the same dtype")
         heads = k.shape[1]
-        _need(v.shape == k.shape, "k and v must have the same shape")
-        _need(k.dim() == 3 and k.shape[0] == T and k.shape[2] == D, f"k must be [{T}][heads][{D}], got {tuple(k.shape)}")
-        _need(k.dtype == lead.dtype and v.dtype == lead.dtype, "q, k and v must have the same dtype")
-        _inner("k", k)
-        _inner("v", v)
-        _whole("slots", slots, torch.int32, (T,))
+        if k.shape != (T, heads, D):
+            raise ValueError(f"k must be [{T}][heads][{D}], got {tuple(k.shape)}")
+        ks, vs = _strides("k", k), _strides("v", v)
+        _whole("slots", slots, _I32, (T,))
         desc = cache.described()
-        _need((desc.heads, desc.head_dim) == (heads, D), f"cache heads {(desc.heads, desc.head_dim)} do not match k {(heads, D)}")
-        kst = (k.stride(0), k.stride(1), v.stride(0), v.stride(1))
-    q_heads, qst, ost = 0, (0, 0), (0, 0)
+        if desc.heads != heads or desc.head_dim != D:
+            raise ValueError(f"cache heads {(desc.heads, desc.head_dim)} do not match k {(heads, D)}")
+        of_cache = (cache.k, cache.v, cache.k_scale, cache.v_scale)
+    else:
+        _need(k is None and v is None and cache is None, "k, v, slots and cache come together")
+        slots, of_cache, ks, vs = None, (), (0, 0), (0, 0)
     if q is not None:
         q_heads = q.shape[1]
-        _inner("q", q)
+        qs = _strides("q", q)
         if q_out is None:
             q_out = torch.empty((T, q_heads, D), dtype=q.dtype, device=q.device)
-        _need(q_out.shape == q.shape and q_out.dtype == q.dtype, "q_out must be like q")
-        _inner("q_out", q_out)
-        qst, ost = q.stride()[:2], q_out.stride()[:2]
-    rot, rscale, rflags, freqs = 0, 1.0, 0, None
+        elif q_out.shape != q.shape or q_out.dtype is not q.dtype:
+            raise ValueError("q_out must be like q")
+        os = _strides("q_out", q_out)
+    else:
+        q_out, qs, os = None, (0, 0), (0, 0)
     if rotary is not None:
         freqs = rotary.freqs
-        _need(freqs.dim() == 1 and 2 * freqs.numel() <= D, f"rotary.freqs must hold at most {D // 2} frequencies")
-        _whole("rotary.freqs", freqs, torch.float64, (freqs.numel(),))
-        _whole("positions", positions, torch.int32, (T,))
-        rot, rscale, rflags = 2 * freqs.numel(), rotary.scale, SPEC_ROPE_INTERLEAVED if rotary.interleaved else 0
+        rot = 2 * freqs.numel()
+        _need(rot <= D, f"rotary.freqs must hold at most {D // 2} frequencies")
+        _whole("rotary.freqs", freqs, _F64, (rot // 2,))
+        _whole("positions", positions, _I32, (T,))
+        rscale, rflags = rotary.scale, SPEC_ROPE_INTERLEAVED if rotary.interleaved else 0
+    else:
+        positions = None
     if status is not None:
-        _whole("status", status, torch.int32, (T,))
-    dev = _same_device(q=q, q_out=q_out if q is not None else None, k=k, v=v, positions=positions if rot else None,
-                       slots=slots if k is not None else None, freqs=freqs, status=status,
-                       cache=cache.k if cache else None, cache_v=cache.v if cache else None,
-                       k_scale=cache.k_scale if cache else None, v_scale=cache.v_scale if cache else None)
-    _call("spec_kv_append", dev, stream, _data(q), *qst, _data(q_out) if q is not None else None, *ost, _data(k), *kst[:2],
-          _data(v), *kst[2:], _HALF[lead.dtype], T, q_heads, heads, D, _data(positions) if rot else None,
-          _data(slots) if k is not None else None, _data(freqs), rot, rscale, rflags,
-          ctypes.byref(desc) if desc else None, _data(status))
-    return q_out if q is not None else None
+        _whole("status", status, _I32, (T,))
+    dev = lead.get_device()
+    _on_one_device(dev, (lead, q_out, k, v, positions, slots, freqs, status, *of_cache))
+    _call("spec_kv_append", dev, stream, _data(q), qs[0], qs[1], _data(q_out), os[0], os[1], _data(k), ks[0], ks[1],
+          _data(v), vs[0], vs[1], code, T, q_heads, heads, D, _data(positions), _data(slots), _data(freqs), rot, rscale,
+          rflags, None if desc is None else ctypes.byref(desc), _data(status))
+    return q_out
 
 
+@functools.lru_cache(maxsize=1024)
 def spec_prefix_attention_workspace_bytes(R: int, G: int, q_heads: int, heads: int, head_dim: int,
                                           max_prefix: int, max_suffix: int) -> int:
     return int(load().cdll.spec_prefix_attention_workspace_bytes(R, G, q_heads, heads, head_dim, max_prefix, max_suffix))
@@ -758,46 +782,57 @@ def spec_prefix_attention(q: torch.Tensor, cache: KVCache, page_table: Optional[
     (page_table [G][max_pages], prefix_len [G]) and its own suffix_slots [R][max_suffix], suffix_len [R].  scale:
     head_dim^-0.5 unless given.  Returns (out, lse); lse [R][q_heads] float32 with want_lse, else None.  Rows
     outside every group (padding) keep what out and lse held, so give both where there are such rows."""
-    _need(q.dim() == 3 and q.dtype in _HALF, "q must be [R][q_heads][head_dim] in bf16 or fp16")
+    code = _HALF.get(q.dtype)
+    if q.dim() != 3 or code is None:
+        raise ValueError("q must be [R][q_heads][head_dim] in bf16 or fp16")
     R, Hq, D = q.shape
-    _inner("q", q)
+    qs = _strides("q", q)
     desc = cache.described()
-    _need(desc.head_dim == D and desc.heads >= 1 and Hq % desc.heads == 0,
-          f"cache heads {(desc.heads, desc.head_dim)} do not serve q {(Hq, D)}")
-    _need(row_start.dim() == 1 and row_start.numel() >= 2, "row_start must be [G+1]")
+    heads = desc.heads
+    if desc.head_dim != D or heads < 1 or Hq % heads:
+        raise ValueError(f"cache heads {(heads, desc.head_dim)} do not serve q {(Hq, D)}")
     G = row_start.numel() - 1
-    _whole("row_start", row_start, torch.int32, (G + 1,))
+    if G < 1:
+        raise ValueError("row_start must be [G+1]")
+    _whole("row_start", row_start, _I32, (G + 1,))
     pages = S = 0
     if page_table is not None:
-        _need(page_table.dim() == 2, "page_table must be [G][max_pages]")
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [G][max_pages]")
         pages = page_table.shape[1]
-        _whole("page_table", page_table, torch.int32, (G, pages))
-        _whole("prefix_len", prefix_len, torch.int32, (G,))
+        _whole("page_table", page_table, _I32, (G, pages))
+        _whole("prefix_len", prefix_len, _I32, (G,))
+    else:
+        prefix_len = None
     if suffix_slots is not None:
-        _need(suffix_slots.dim() == 2, "suffix_slots must be [R][max_suffix]")
+        if suffix_slots.dim() != 2:
+            raise ValueError("suffix_slots must be [R][max_suffix]")
         S = suffix_slots.shape[1]
-        _whole("suffix_slots", suffix_slots, torch.int32, (R, S))
-        _whole("suffix_len", suffix_len, torch.int32, (R,))
-    dev = q.device
+        _whole("suffix_slots", suffix_slots, _I32, (R, S))
+        _whole("suffix_len", suffix_len, _I32, (R,))
+    else:
+        suffix_len = None
     if out is None:
-        out = torch.empty((R, Hq, D), dtype=q.dtype, device=dev)
-    _need(out.shape == q.shape and out.dtype == q.dtype, "out must be like q")
-    _inner("out", out)
-    if lse is None and want_lse:
-        lse = torch.empty((R, Hq), dtype=torch.float32, device=dev)
+        out = torch.empty((R, Hq, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype is not q.dtype:
+        raise ValueError("out must be like q")
+    os = _strides("out", out)
     if lse is not None:
-        _whole("lse", lse, torch.float32, (R, Hq))
+        _whole("lse", lse, _F32, (R, Hq))
+    elif want_lse:
+        lse = torch.empty((R, Hq), dtype=_F32, device=q.device)
     if workspace is None:
-        workspace = torch.empty(max(spec_prefix_attention_workspace_bytes(R, G, Hq, desc.heads, D, pages * desc.page_size, S), 1),
-                                dtype=torch.uint8, device=dev)
-    _workspace(workspace)
-    _same_device(q=q, cache=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale, page_table=page_table,
-                 prefix_len=prefix_len, row_start=row_start, suffix_slots=suffix_slots, suffix_len=suffix_len, out=out,
-                 lse=lse, workspace=workspace)
-    _call("spec_prefix_attention", dev, stream, _data(q), q.stride(0), q.stride(1), _HALF[q.dtype], R, Hq,
-          ctypes.byref(desc), G, _data(row_start), _data(page_table), pages, _data(prefix_len), _data(suffix_slots), S,
-          _data(suffix_len), D ** -0.5 if scale is None else scale, _data(out), out.stride(0), out.stride(1), _data(lse),
-          _data(workspace), workspace.numel())
+        workspace = torch.empty(spec_prefix_attention_workspace_bytes(R, G, Hq, heads, D, pages * desc.page_size, S),
+                                dtype=_U8, device=q.device)
+    else:
+        _workspace(workspace)
+    dev = q.get_device()
+    _on_one_device(dev, (q, cache.k, cache.v, cache.k_scale, cache.v_scale, page_table, prefix_len, row_start,
+                         suffix_slots, suffix_len, out, lse, workspace))
+    _call("spec_prefix_attention", dev, stream, q.data_ptr(), qs[0], qs[1], code, R, Hq, ctypes.byref(desc), G,
+          row_start.data_ptr(), _data(page_table), pages, _data(prefix_len), _data(suffix_slots), S, _data(suffix_len),
+          D ** -0.5 if scale is None else scale, out.data_ptr(), os[0], os[1], _data(lse), workspace.data_ptr(),
+          workspace.numel())
     return out, lse
 
 

@@ -441,25 +441,17 @@ __device__ __forceinline__ void prefix_piece(const Args& a, int index, char* lds
         if (wk > 0) return;
 #pragma unroll
         for (int n = 0; n < MB; ++n) {
-            float m = st.m[n];
-            float2 ml[WK - 1];
-#pragma unroll
+#pragma unroll 1
             for (int w = 0; w < WK - 1; ++w) {
-                ml[w] = mm[((w * WQ + wq) * MB + n) * 16 + (lane & 15)];
-                m = fmaxf(m, ml[w].x);
-            }
-            float f = exp2_fast(st.m[n] - m);
-            st.m[n] = m;
-            st.l[n] *= f;
-#pragma unroll
-            for (int b = 0; b < DP / 16; ++b) st.o[n][b] *= f;
-#pragma unroll
-            for (int w = 0; w < WK - 1; ++w) {
-                f = exp2_fast(ml[w].x - m);
-                st.l[n] += ml[w].y * f;
+                const int at = (w * WQ + wq) * MB + n;
+                const float2 ml = mm[at * 16 + (lane & 15)];
+                const float m = fmaxf(st.m[n], ml.x);
+                const float keep = exp2_fast(st.m[n] - m), f = exp2_fast(ml.x - m);
+                st.m[n] = m;
+                st.l[n] = st.l[n] * keep + ml.y * f;
 #pragma unroll
                 for (int b = 0; b < DP / 16; ++b)
-                    st.o[n][b] += *reinterpret_cast<const f32x4*>(mo + (((((w * WQ + wq) * MB + n) * (DP / 16)) + b) * 64 + lane) * 4) * f;
+                    st.o[n][b] = st.o[n][b] * keep + *reinterpret_cast<const f32x4*>(mo + ((at * (DP / 16) + b) * 64 + lane) * 4) * f;
             }
         }
     }
@@ -563,7 +555,7 @@ __device__ __forceinline__ void suffix_wave(const Args& a, int64_t task, char* l
 }
 
 template <typename T, typename C, int DP, int MB, int WQ>
-__global__ __launch_bounds__(kThreads) void attention_pieces_kernel(Args a) {
+__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attention_pieces_kernel(Args a) {
     constexpr int kSuffixBytes = 4 * 32 * DP * 2;
     constexpr int kPieceBytes = PieceLds<T, C, DP, MB, WQ>::kBytes;
     __shared__ __align__(16) char lds[kPieceBytes > kSuffixBytes ? kPieceBytes : kSuffixBytes];
