@@ -349,16 +349,18 @@ __device__ __forceinline__ void prefix_piece(const Args& a, int index, char* lds
     const int chunk = tid % kChunks, key0 = tid / kChunks;
     raw kr[kLoads], vr[kLoads];
 
-    // where the keys of the step at t lie, by the first KT threads
-    auto look_up = [&](int t, int buf) {
+    // Where the keys of the step at t lie, by the first KT threads: the page is asked for ahead of the
+    // keys and values loaded in the same step (loads return in order, so what waits for the page
+    // does not wait for those), the offset is left in LDS after the step's products.
+    auto page_of = [&](int t) {
+        const int at = t + tid;
+        return tid < KT && at < pc.end ? table[a.page_shift >= 0 ? at >> a.page_shift : at / a.cache.page_size] : -1;
+    };
+    auto leave = [&](int t, int page, int buf) {
         if (tid < KT) {
             const int at = t + tid;
-            int64_t o = -1;
-            if (at < pc.end) {
-                const int page = a.page_shift >= 0 ? at >> a.page_shift : at / a.cache.page_size;
-                o = slot_offset(a, table[page], at - page * a.cache.page_size);
-            }
-            offs[buf][tid] = o;
+            const int in_page = a.page_shift >= 0 ? at & (a.cache.page_size - 1) : at % a.cache.page_size;
+            offs[buf][tid] = slot_offset(a, page, in_page);
         }
     };
     auto load = [&](int buf) {
@@ -377,10 +379,11 @@ __device__ __forceinline__ void prefix_piece(const Args& a, int index, char* lds
     char* kl = lds;
     char* vl = lds + L::kTileBytes;
 
-    look_up(pc.begin, 0);
+    leave(pc.begin, page_of(pc.begin), 0);
+    int page = page_of(pc.begin + KT);
     __syncthreads();
     load(0);
-    look_up(pc.begin + KT, 1);
+    leave(pc.begin + KT, page, 1);
     int buf = 0;
     for (int t = pc.begin; t < pc.end; t += KT, buf ^= 1) {
         // which of the wave's keys exist (read before the offsets are overwritten)
@@ -397,13 +400,12 @@ __device__ __forceinline__ void prefix_piece(const Args& a, int index, char* lds
         }
         __syncthreads();
         if (t + KT < pc.end) {
+            page = page_of(t + 2 * KT);
             load(buf ^ 1);
-            look_up(t + 2 * KT, buf);
         }
-        if (nb == 0) continue;
 #pragma unroll
         for (int sub = 0; sub < KT / (32 * WK); ++sub) {
-            if (valid[sub] == 0) continue;
+            if (nb == 0 || valid[sub] == 0) continue;
             const int key = (sub * WK + wk) * 32;
             f32x4 s[MB][2];
 #pragma unroll
@@ -418,6 +420,7 @@ __device__ __forceinline__ void prefix_piece(const Args& a, int index, char* lds
                 }
             weigh<T, MB, MB, DP>(st, s, valid[sub], c, vl + key * DP * 2);
         }
+        leave(t + 2 * KT, page, buf);
     }
 #pragma unroll
     for (int n = 0; n < MB; ++n) st.l[n] = sum_over_quarters(st.l[n]);
