@@ -572,41 +572,79 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attention_pieces_
 }
 
 // ------------------------------------------------------------------------------------------
-// The join: DP / 4 lanes per (row, query head), four elements each.
+// The join: DP / 4 lanes per (row, query head), four elements each.  The lanes first take the
+// maxima and sums, one part per lane, so that the parts' outputs can then be asked for without
+// waiting for one another.  With few rows (`ways`) a whole workgroup shares one pair and each of
+// its groups of lanes takes every kWays-th part.
 // ------------------------------------------------------------------------------------------
 template <typename T, int DP>
-__global__ __launch_bounds__(kThreads) void attention_join_kernel(Args a, int mt) {
-    constexpr int kLanes = DP / 4;
-    const int lane = threadIdx.x % kLanes;
-    const int64_t pair = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-    if (pair >= (int64_t)a.R * a.q_heads) return;
-    const int r = (int)(pair / a.q_heads), h = (int)(pair % a.q_heads), kvh = h / a.per;
-    const int g = group_of(a, r, lane, kLanes);
-    if (g < 0) return;
+__global__ __launch_bounds__(kThreads) void attention_join_kernel(Args a, int mt, int shared) {
+    constexpr int kLanes = DP / 4, kWays = kThreads / kLanes;
+    __shared__ f32x4 meet[kWays][kLanes];
+    const int lane = threadIdx.x % kLanes, set = threadIdx.x / kLanes;
+    const int ways = shared ? kWays : 1, way = shared ? set : 0;
+    const int64_t pair = shared ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kWays + set;
+    const bool there = pair < (int64_t)a.R * a.q_heads;
+    const int r = there ? (int)(pair / a.q_heads) : 0, h = there ? (int)(pair % a.q_heads) : 0, kvh = h / a.per;
+    const int g = there ? group_of(a, r, lane, kLanes) : -1;
     const int d = lane * 4;
     float m = kNone, l = 0.0f;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto add = [&](float2 ml, const float* from) {
-        const float top = fmaxf(m, ml.x);
-        const float keep = exp2_fast(m - top), f = exp2_fast(ml.x - top);
+    if (g >= 0) {
+        // part 0 is the suffix, then the pieces along the prefix
+        const int first = a.max_suffix ? 1 : 0;
+        int parts = first;
+        int64_t at0 = 0, step = 0;
+        if (a.slots) {
+            const int2 rows = rows_of(a, g), span = a.groups[g];
+            const int q = (r - rows.x) * a.per + h - kvh * a.per;
+            const int tiles = (rows.y * a.per + mt - 1) / mt, tile = q / mt;
+            at0 = ((int64_t)(span.x + tile) * a.heads + kvh) * mt + (q - tile * mt);
+            step = (int64_t)tiles * a.heads * mt;
+            parts += span.y;
+        }
+        const auto ml_of = [&](int p) { return p < first ? a.suffix_ml[pair] : a.piece_ml[at0 + (p - first) * step]; };
+        const auto o_of = [&](int p) { return (p < first ? a.suffix_o + pair * a.D : a.piece_o + (at0 + (p - first) * step) * a.D) + d; };
+        for (int p = lane; p < parts; p += kLanes) {
+            const float2 ml = ml_of(p);
+            const float top = fmaxf(m, ml.x);
+            l = l * exp2_fast(m - top) + ml.y * exp2_fast(ml.x - top);
+            m = top;
+        }
+        float top = m;
+#pragma unroll
+        for (int s = 1; s < kLanes; s <<= 1) top = fmaxf(top, __shfl_xor(top, s));
+        l *= exp2_fast(m - top);
+#pragma unroll
+        for (int s = 1; s < kLanes; s <<= 1) l += __shfl_xor(l, s);
         m = top;
-        l = l * keep + ml.y * f;
-        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (d < a.D) x = *reinterpret_cast<const f32x4*>(from + d);
-        o = o * keep + x * f;
-    };
-    if (a.max_suffix) add(a.suffix_ml[pair], a.suffix_o + pair * a.D);
-    if (a.slots) {
-        const int2 rows = rows_of(a, g), span = a.groups[g];
-        const int q = (r - rows.x) * a.per + h - kvh * a.per;
-        const int tiles = (rows.y * a.per + mt - 1) / mt, tile = q / mt;
-        for (int s = 0; s < span.y; ++s) {
-            const int64_t at = ((int64_t)(span.x + s * tiles + tile) * a.heads + kvh) * mt + (q - tile * mt);
-            add(a.piece_ml[at], a.piece_o + at * a.D);
+        if (d < a.D) {
+            int p = way;
+            for (; p + 3 * ways < parts; p += 4 * ways) {
+                f32x4 x[4];
+                float f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = *reinterpret_cast<const f32x4*>(o_of(p + e * ways));
+                    f[e] = ml_of(p + e * ways).x;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o += x[e] * exp2_fast(f[e] - m);
+            }
+            for (; p < parts; p += ways) o += *reinterpret_cast<const f32x4*>(o_of(p)) * exp2_fast(ml_of(p).x - m);
         }
     }
+    if (shared) {
+        meet[set][lane] = o;
+        __syncthreads();
+        if (set > 0 || g < 0) return;
+#pragma unroll
+        for (int w = 1; w < kWays; ++w) o += meet[w][lane];
+    } else if (g < 0) {
+        return;
+    }
     if (d < a.D) {
-        const float f = l == 0.0f ? 0.0f : (a.cache.v_scale ? a.cache.v_scale[kvh] : 1.0f) / l;
+        const float f = (a.cache.v_scale ? a.cache.v_scale[kvh] : 1.0f) / l;
         typedef T v4 __attribute__((ext_vector_type(4)));
         v4 y;
 #pragma unroll
@@ -621,9 +659,11 @@ static void launch_tile(const Args& a, hipStream_t stream) {
     const unsigned blocks = (unsigned)(a.slots * a.heads + a.suffix_blocks);
     if (blocks)
         hipLaunchKernelGGL((attention_pieces_kernel<T, C, DP, MB, WQ>), dim3(blocks), dim3(kThreads), 0, stream, a);
+    // few rows against a long prefix have many pieces each: a workgroup per pair then
     const int64_t per = kThreads / (DP / 4), pairs = (int64_t)a.R * a.q_heads;
-    hipLaunchKernelGGL((attention_join_kernel<T, DP>), dim3((unsigned)((pairs + per - 1) / per)), dim3(kThreads), 0, stream, a,
-                       16 * MB * WQ);
+    const int shared = pairs <= 1024 && a.slots / a.G > 8;
+    hipLaunchKernelGGL((attention_join_kernel<T, DP>), dim3((unsigned)(shared ? pairs : (pairs + per - 1) / per)),
+                       dim3(kThreads), 0, stream, a, 16 * MB * WQ, shared);
 }
 
 template <typename T, typename C>
