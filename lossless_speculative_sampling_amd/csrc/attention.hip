@@ -106,17 +106,25 @@ __device__ __forceinline__ float sum_over_quarters(float x) {
 }
 
 // ------------------------------------------------------------------------------------------
-// LDS tiles: rows of DP elements, 16-byte chunks exchanged within a row so that the lanes of one
-// read fall on different banks: keys are read 8 rows at a time at one chunk, values 4 rows at a
-// time at one pair of chunks.
+// LDS tiles: rows of DP elements, 16-byte chunks exchanged within a row so that what one read takes
+// at once (of keys one chunk of 16 rows, of values a pair of chunks of 8 rows) covers all banks.
+// Two rows of 64 elements share a span of the banks, so there the row's second bit on counts.
 // ------------------------------------------------------------------------------------------
 template <int DP>
 __device__ __forceinline__ int k_at(int key, int chunk) {
-    return key * DP * 2 + ((chunk ^ (key & 7)) << 4);
+    return key * DP * 2 + ((chunk ^ (DP == 64 ? (key >> 1) & 7 : key & 15)) << 4);
 }
 template <int DP>
 __device__ __forceinline__ int v_at(int key, int chunk) {
-    return key * DP * 2 + ((chunk ^ ((key & 3) << 1)) << 4);
+    return key * DP * 2 + ((chunk ^ (DP == 64 ? key & 6 : (key & 7) << 1)) << 4);
+}
+
+// The exchanges touch bits 4 to 7 of an address, chunks come in by exclusive or, so one address serves
+// all reads of a row.  Kept opaque, or the compiler holds each of them in a register of its own
+// through the loop, and those are worth more than an instruction.
+__device__ __forceinline__ int again(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
 }
 
 __device__ __forceinline__ s16x4 transposed4(const char* p) {
@@ -124,7 +132,8 @@ __device__ __forceinline__ s16x4 transposed4(const char* p) {
 }
 
 // The running softmax of a wave's query blocks: lane l holds query l % 16 of each block, of the
-// output the elements 16 b + 4 (l / 16) .. + 3 of every block b, of the sum its own keys' part.
+// output the elements 16 b + 4 (l / 16) .. + 3 of every block b, of the sum its own keys' part (of the
+// weights before their rounding: the log of the sum is an output too).
 template <int MB, int DP>
 struct State {
     f32x4 o[MB][DP / 16];
@@ -143,47 +152,84 @@ struct State {
 
 // Scores of 32 keys (s[i][0]: keys 0..15, s[i][1]: 16..31; lane l has keys 4 (l / 16) .. + 3 of each)
 // into weights, and the product with their values from `vl`.  `valid`: which keys exist.
-template <typename T, int NB, int MB, int DP>
-__device__ __forceinline__ void weigh(State<MB, DP>& st, f32x4 (&s)[NB][2], uint32_t valid, float c, const char* vl) {
+template <typename T, int MB, int DP>
+__device__ __forceinline__ void weigh(State<MB, DP>& st, f32x4 (&s)[MB][2], uint32_t valid, float c, const char* vl) {
     const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, i = lane & 15;
     if (valid != 0xffffffffu) {
+        const uint32_t mine = valid >> (g * 4);
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+        for (int n = 0; n < MB; ++n)
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (!((valid >> (kb * 16 + g * 4 + e)) & 1)) s[n][kb][e] = -__builtin_inff();
+                    s[n][kb][e] = (mine >> (kb * 16 + e)) & 1 ? s[n][kb][e] : -__builtin_inff();
     }
-    s16x8 p[NB];
+    float top[MB];
+    bool up = false;
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-        float top = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
-                          fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
-        if (__any(top * c > st.m[n] + kSlack)) {
-            const float m = fmaxf(st.m[n], max_over_quarters(top) * c);
+    for (int n = 0; n < MB; ++n) {
+        // (the kind of maximum that passes NaN on: a query that meets one is NaN whatever its reference)
+        float x = s[n][0][0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) x = __builtin_elementwise_maximum(x, s[n][e >> 2][e & 3]);
+        top[n] = x * c;
+        up = up || top[n] > st.m[n] + kSlack;
+    }
+    if (__any(up)) {
+#pragma unroll
+        for (int n = 0; n < MB; ++n) {
+            const float m = fmaxf(st.m[n], max_over_quarters(top[n]));
             const float f = exp2_fast(st.m[n] - m);
             st.m[n] = m;
             st.l[n] *= f;
 #pragma unroll
             for (int b = 0; b < DP / 16; ++b) st.o[n][b] *= f;
         }
+    }
+    s16x8 p[MB];
+#pragma unroll
+    for (int n = 0; n < MB; ++n) {
         float w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = exp2_fast(fmaf(s[n][e >> 2][e & 3], c, -st.m[n]));
-        st.l[n] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
         p[n] = narrow8<T>(w);
+        st.l[n] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
     }
     // lane i of a quarter reads row 4 g + i / 4 at elements 4 (i % 4) .. + 3 of the block and gets
     // column i of the four rows
+    const int base = again(v_at<DP>(g * 4 + (i >> 2), (i & 3) >> 1) + (i & 1) * 8);
 #pragma unroll
     for (int b = 0; b < DP / 16; ++b) {
-        const char* at = vl + v_at<DP>(g * 4 + (i >> 2), b * 2 + ((i & 3) >> 1)) + (i & 1) * 8;
+        const char* at = vl + (base ^ ((b & 7) << 5)) + (b >> 3) * 256;  // = v_at(.., 2 b + ..)
         const s16x4 lo = transposed4(at), hi = transposed4(at + 16 * DP * 2);
         const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-        for (int n = 0; n < NB; ++n) st.o[n][b] = mma<T>(v, p[n], st.o[n][b]);
+        for (int n = 0; n < MB; ++n) st.o[n][b] = mma<T>(v, p[n], st.o[n][b]);
+        if (DP > 128 && b % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // few reads ahead: registers
     }
+}
+
+// A wave's query blocks against 32 keys of LDS.
+template <typename T, int MB, int DP>
+__device__ __forceinline__ void step(State<MB, DP>& st, const s16x8 (&q)[MB][DP / 32], uint32_t valid, float c, const char* kl,
+                                     const char* vl) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int base = again(k_at<DP>(lane & 15, lane >> 4));
+    f32x4 s[MB][2];
+#pragma unroll
+    for (int n = 0; n < MB; ++n) s[n][0] = s[n][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int kk = 0; kk < DP / 32; ++kk) {
+            const s16x8 x = *reinterpret_cast<const s16x8*>(  // = k_at(16 kb + .., 4 kk + ..)
+                kl + (base ^ ((kk & 3) << 6)) + (kk >> 2) * 256 + kb * 16 * DP * 2);
+#pragma unroll
+            for (int n = 0; n < MB; ++n) s[n][kb] = mma<T>(x, q[n][kk], s[n][kb]);
+            if (DP > 128 && kk % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // few reads ahead: registers
+        }
+    weigh<T, MB, DP>(st, s, valid, c, vl);
 }
 
 // A cache slot's offset in elements, or -1 where there is no token.
@@ -296,12 +342,12 @@ __device__ __forceinline__ Piece find_piece(const Args& a, int x, bool leave, Pl
     return sh.piece;
 }
 
-// Keys a workgroup takes per step: 32 per wave that stands alone over its keys, at least 64.
-constexpr int keys_of(int wq) { return wq == 1 ? 128 : 64; }
+// Keys a workgroup takes per step, as far as the registers that hold the next step's go.
+constexpr int keys_of(int dp) { return dp > 128 ? 32 : 64; }
 
 template <typename T, typename C, int DP, int MB, int WQ>
 struct PieceLds {
-    static constexpr int KT = keys_of(WQ);
+    static constexpr int KT = keys_of(DP);
     static constexpr int kTileBytes = KT * DP * 2;
     static constexpr int kWK = 4 / WQ;
     // the waves over the same queries meet in the same memory at the end
@@ -318,8 +364,9 @@ __device__ __forceinline__ void prefix_piece(const Args& a, int index, char* lds
     constexpr int kStep = kThreads / kChunks;          // keys between a thread's loads
     typedef typename Raw<T, C>::type raw;
     __shared__ PlanShared plan;
-    __shared__ int64_t offs[2][KT];
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
+    __shared__ int64_t offs[2][KT];        // where a key lies (a key that does not exist: at the start)
+    __shared__ uint32_t exists[2][KT / 32];  // which keys exist
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wq = wave % WQ, wk = wave / WQ;
     const int kvh = index % a.heads;
     const Piece pc = find_piece<MT, KT>(a, index / a.heads, index == 0, plan);
@@ -343,10 +390,10 @@ __device__ __forceinline__ void prefix_piece(const Args& a, int index, char* lds
         load_queries<T, DP>(a, q[n], pc.first + row, kvh * a.per + h, there, negate);
     }
 
-    const C* kc = static_cast<const C*>(a.cache.k) + (int64_t)kvh * a.cache.head_stride;
-    const C* vc = static_cast<const C*>(a.cache.v) + (int64_t)kvh * a.cache.head_stride;
     const int32_t* table = a.table + (int64_t)pc.g * a.max_pages;
     const int chunk = tid % kChunks, key0 = tid / kChunks;
+    const bool inside = chunk * 8 < a.D;  // a chunk past head_dim is zero in LDS
+    const int chunk0 = inside ? chunk * 8 : 0;
     raw kr[kLoads], vr[kLoads];
 
     // Where the keys of the step at t lie, by the first KT threads: the page is asked for ahead of the
@@ -360,20 +407,22 @@ __device__ __forceinline__ void prefix_piece(const Args& a, int index, char* lds
         if (tid < KT) {
             const int at = t + tid;
             const int in_page = a.page_shift >= 0 ? at & (a.cache.page_size - 1) : at % a.cache.page_size;
-            offs[buf][tid] = slot_offset(a, page, in_page);
+            const int64_t o = slot_offset(a, page, in_page);
+            offs[buf][tid] = (o < 0 ? 0 : o) * (int64_t)sizeof(C);
+            const uint64_t there = __ballot(o >= 0);
+            if ((lane & 31) == 0) exists[buf][tid >> 5] = (uint32_t)(there >> lane);
         }
     };
+    // (of a key that does not exist the cache's first token is loaded: its score is masked, its value
+    // zeroed on the way into LDS)
+    const char* kc = reinterpret_cast<const char*>(static_cast<const C*>(a.cache.k) + (int64_t)kvh * a.cache.head_stride + chunk0);
+    const char* vc = reinterpret_cast<const char*>(static_cast<const C*>(a.cache.v) + (int64_t)kvh * a.cache.head_stride + chunk0);
     auto load = [&](int buf) {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const int64_t o = offs[buf][key0 + j * kStep];
-            raw x = {}, y = {};
-            if (o >= 0 && chunk * 8 < a.D) {
-                x = *reinterpret_cast<const raw*>(kc + o + chunk * 8);
-                y = *reinterpret_cast<const raw*>(vc + o + chunk * 8);
-            }
-            kr[j] = x;
-            vr[j] = y;
+            kr[j] = *reinterpret_cast<const raw*>(kc + o);
+            vr[j] = *reinterpret_cast<const raw*>(vc + o);
         }
     };
     char* kl = lds;
@@ -386,12 +435,26 @@ __device__ __forceinline__ void prefix_piece(const Args& a, int index, char* lds
     leave(pc.begin + KT, page, 1);
     int buf = 0;
     for (int t = pc.begin; t < pc.end; t += KT, buf ^= 1) {
-        // which of the wave's keys exist (read before the offsets are overwritten)
-        uint32_t valid[KT / (32 * WK)];
+        // which keys exist (read before that is overwritten): the wave's own, and whether all do
+        uint32_t valid[KT / (32 * WK)], all = 0xffffffffu;
 #pragma unroll
-        for (int sub = 0; sub < KT / (32 * WK); ++sub)
-            valid[sub] = (uint32_t)__ballot(offs[buf][(sub * WK + wk) * 32 + (lane & 31)] >= 0);
+        for (int w = 0; w < KT / 32; ++w) all &= __builtin_amdgcn_readfirstlane(exists[buf][w]);
+#pragma unroll
+        for (int sub = 0; sub < KT / (32 * WK); ++sub) valid[sub] = __builtin_amdgcn_readfirstlane(exists[buf][sub * WK + wk]);
+        uint32_t mine = 0xffffffffu;  // of this thread's, by load
+        if (all != 0xffffffffu) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int key = key0 + j * kStep;
+                if (!((exists[buf][key >> 5] >> (key & 31)) & 1)) mine &= ~(1u << j);
+            }
+        }
         __syncthreads();  // the last step's tile has been read
+        if (all != 0xffffffffu || a.D != DP) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)
+                if (!inside || !((mine >> j) & 1)) kr[j] = vr[j] = raw{};
+        }
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const int key = key0 + j * kStep;
@@ -405,20 +468,8 @@ __device__ __forceinline__ void prefix_piece(const Args& a, int index, char* lds
         }
 #pragma unroll
         for (int sub = 0; sub < KT / (32 * WK); ++sub) {
-            if (nb == 0 || valid[sub] == 0) continue;
             const int key = (sub * WK + wk) * 32;
-            f32x4 s[MB][2];
-#pragma unroll
-            for (int n = 0; n < MB; ++n) s[n][0] = s[n][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                for (int kk = 0; kk < DP / 32; ++kk) {
-                    const s16x8 x = *reinterpret_cast<const s16x8*>(kl + k_at<DP>(key + kb * 16 + (lane & 15), kk * 4 + (lane >> 4)));
-#pragma unroll
-                    for (int n = 0; n < MB; ++n) s[n][kb] = mma<T>(x, q[n][kk], s[n][kb]);
-                }
-            weigh<T, MB, MB, DP>(st, s, valid[sub], c, vl + key * DP * 2);
+            if (nb > 0 && valid[sub] != 0) step<T, MB, DP>(st, q, valid[sub], c, kl + key * DP * 2, vl + key * DP * 2);
         }
         leave(t + 2 * KT, page, buf);
     }
@@ -513,43 +564,66 @@ __device__ __forceinline__ void suffix_wave(const Args& a, int64_t task, char* l
     State<1, DP> st;
     st.clear();
     for (int t = 0; t < S; t += 32) {
+        // keys and values are asked for together, or 16 by 16 where that is too many registers; a slot
+        // that holds no token and the elements past head_dim are read from where there are some, and
+        // taken as zeros
+        constexpr bool kTogether = DP <= 128;
         raw x[2][DP / 32], y[2][DP / 32];
+        int64_t o[2];
         uint32_t valid = 0;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            const int at = t + kb * 16 + i;
-            const int64_t o = at < S ? slot_offset(a, list[at]) : -1;
-            valid |= ((uint32_t)__ballot(o >= 0) & 0xffffu) << (kb * 16);
+        const auto fetch = [&](const C* from, int kb, raw (&to)[DP / 32]) {
+            const C* p = from + (o[kb] >= 0 ? o[kb] : 0);
 #pragma unroll
             for (int kk = 0; kk < DP / 32; ++kk) {
                 const int d = kk * 32 + g * 8;
-                x[kb][kk] = raw{};
-                y[kb][kk] = raw{};
-                if (o >= 0 && d < a.D) {
-                    x[kb][kk] = *reinterpret_cast<const raw*>(kc + o + d);
-                    y[kb][kk] = *reinterpret_cast<const raw*>(vc + o + d);
-                }
+                to[kk] = *reinterpret_cast<const raw*>(p + (d < a.D ? d : 0));
             }
+        };
+        const auto taken = [&](const raw& r, int kb, int kk) {
+            const s16x8 w = Raw<T, C>::widen(r);
+            return o[kb] >= 0 && kk * 32 + g * 8 < a.D ? w : s16x8{};
+        };
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            const int at = t + kb * 16 + i;
+            o[kb] = at < S ? slot_offset(a, list[at]) : -1;
+            valid |= ((uint32_t)__ballot(o[kb] >= 0) & 0xffffu) << (kb * 16);
         }
         if (valid == 0) continue;
+        if (kTogether) {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                fetch(kc, kb, x[kb]);
+                fetch(vc, kb, y[kb]);
+            }
+        }
         f32x4 s[1][2];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
+            if (!kTogether) {
+                __builtin_amdgcn_sched_barrier(0);
+                fetch(kc, kb, x[kb]);
+            }
             s[0][kb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
+            for (int kk = 0; kk < DP / 32; ++kk) s[0][kb] = mma<T>(taken(x[kb][kk], kb, kk), q[0][kk], s[0][kb]);
+            if (!kTogether) {
+                __builtin_amdgcn_sched_barrier(0);
+                fetch(vc, kb, y[kb]);
+            }
+#pragma unroll
             for (int kk = 0; kk < DP / 32; ++kk) {
-                s[0][kb] = mma<T>(Raw<T, C>::widen(x[kb][kk]), q[0][kk], s[0][kb]);
-                *reinterpret_cast<s16x8*>(lds + v_at<DP>(kb * 16 + i, kk * 4 + g)) = Raw<T, C>::widen(y[kb][kk]);
+                *reinterpret_cast<s16x8*>(lds + v_at<DP>(kb * 16 + i, kk * 4 + g)) = taken(y[kb][kk], kb, kk);
             }
         }
         __builtin_amdgcn_wave_barrier();
-        weigh<T, 1, 1, DP>(st, s, valid, c, lds);
+        weigh<T, 1, DP>(st, s, valid, c, lds);
         __builtin_amdgcn_wave_barrier();
     }
-    st.l[0] = sum_over_quarters(st.l[0]);
+    const float sum = sum_over_quarters(st.l[0]);
     if (h >= a.per) return;
     const int64_t at = (int64_t)r * a.q_heads + kvh * a.per + h;
-    if (g == 0) a.suffix_ml[at] = make_float2(st.m[0], st.l[0]);
+    if (g == 0) a.suffix_ml[at] = make_float2(st.m[0], sum);
 #pragma unroll
     for (int b = 0; b < DP / 16; ++b) {
         const int d = b * 16 + g * 4;
@@ -558,7 +632,7 @@ __device__ __forceinline__ void suffix_wave(const Args& a, int64_t task, char* l
 }
 
 template <typename T, typename C, int DP, int MB, int WQ>
-__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attention_pieces_kernel(Args a) {
+__global__ __launch_bounds__(kThreads, 2) void attention_pieces_kernel(Args a) {
     constexpr int kSuffixBytes = 4 * 32 * DP * 2;
     constexpr int kPieceBytes = PieceLds<T, C, DP, MB, WQ>::kBytes;
     __shared__ __align__(16) char lds[kPieceBytes > kSuffixBytes ? kPieceBytes : kSuffixBytes];
@@ -669,18 +743,12 @@ static void launch_tile(const Args& a, hipStream_t stream) {
 template <typename T, typename C>
 static void launch_typed(const Args& a, const Tile& t, hipStream_t stream) {
     if (a.D > 128) {
-        if (t.mb == 1) launch_tile<T, C, 256, 1, 2>(a, stream);
-        else if (t.wq == 2) launch_tile<T, C, 256, 2, 2>(a, stream);
-        else launch_tile<T, C, 256, 2, 4>(a, stream);
+        launch_tile<T, C, 256, 1, 4>(a, stream);
     } else if (a.D > 64) {
-        if (t.mb == 1) launch_tile<T, C, 128, 1, 1>(a, stream);
-        else if (t.wq == 1) launch_tile<T, C, 128, 2, 1>(a, stream);
-        else if (t.wq == 2) launch_tile<T, C, 128, 2, 2>(a, stream);
+        if (t.mb == 1) launch_tile<T, C, 128, 1, 4>(a, stream);
         else launch_tile<T, C, 128, 2, 4>(a, stream);
     } else {
-        if (t.mb == 1) launch_tile<T, C, 64, 1, 1>(a, stream);
-        else if (t.wq == 1) launch_tile<T, C, 64, 2, 1>(a, stream);
-        else if (t.wq == 2) launch_tile<T, C, 64, 2, 2>(a, stream);
+        if (t.mb == 1) launch_tile<T, C, 64, 1, 4>(a, stream);
         else launch_tile<T, C, 64, 2, 4>(a, stream);
     }
 }
