@@ -329,10 +329,12 @@ __device__ __forceinline__ Piece find_piece(const Args& a, int x, bool leave, Pl
         if (g < a.G && leave) a.groups[g] = make_int2(at, n);
         if (x >= at && x < at + t * n) {
             const int part = (x - at) / t;
+            const int64_t each = ((len + n - 1) / n + KT - 1) / KT * KT;  // the group's stretches alike
+            const int64_t begin = part * each, end = begin + each;
             sh.piece.g = g;
             sh.piece.tile = (x - at) - part * t;
-            sh.piece.begin = (int)(part * stretch);
-            sh.piece.end = (int)(len < (part + 1) * stretch ? len : (part + 1) * stretch);
+            sh.piece.begin = (int)(begin < len ? begin : len);
+            sh.piece.end = (int)(end < len ? end : len);
             sh.piece.first = rows.x;
             sh.piece.rows = rows.y;
         }
