@@ -49,7 +49,8 @@ struct Tile {
 // cost more than idle columns of a matrix instruction), as far as the registers go.
 inline Tile tile_of(int R, int G, int per, int D) {
     const int64_t m = ((int64_t)R * per + G - 1) / G;
-    return m <= 64 || D > 128 ? Tile{1, 4} : Tile{2, 4};
+    if (D > 128) return Tile{1, 4};
+    return m <= 32 ? Tile{1, 2} : m <= 64 ? Tile{2, 2} : Tile{2, 4};
 }
 
 struct Plan {

@@ -742,17 +742,22 @@ static void launch_tile(const Args& a, hipStream_t stream) {
                        dim3(kThreads), 0, stream, a, 16 * MB * WQ, shared);
 }
 
+template <typename T, typename C, int DP>
+static void launch_head(const Args& a, const Tile& t, hipStream_t stream) {
+    if constexpr (DP > 128) {
+        launch_tile<T, C, DP, 1, 4>(a, stream);
+    } else {
+        if (t.mb == 1 && t.wq == 2) launch_tile<T, C, DP, 1, 2>(a, stream);
+        else if (t.wq == 2) launch_tile<T, C, DP, 2, 2>(a, stream);
+        else launch_tile<T, C, DP, 2, 4>(a, stream);
+    }
+}
+
 template <typename T, typename C>
 static void launch_typed(const Args& a, const Tile& t, hipStream_t stream) {
-    if (a.D > 128) {
-        launch_tile<T, C, 256, 1, 4>(a, stream);
-    } else if (a.D > 64) {
-        if (t.mb == 1) launch_tile<T, C, 128, 1, 4>(a, stream);
-        else launch_tile<T, C, 128, 2, 4>(a, stream);
-    } else {
-        if (t.mb == 1) launch_tile<T, C, 64, 1, 4>(a, stream);
-        else launch_tile<T, C, 64, 2, 4>(a, stream);
-    }
+    if (a.D > 128) launch_head<T, C, 256>(a, t, stream);
+    else if (a.D > 64) launch_head<T, C, 128>(a, t, stream);
+    else launch_head<T, C, 64>(a, t, stream);
 }
 
 void launch(const Args& a, const Tile& t, int dtype, hipStream_t stream) {
