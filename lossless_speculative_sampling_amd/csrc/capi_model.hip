@@ -37,9 +37,9 @@ extern "C" {
 
 size_t spec_verify_probs_workspace_bytes(int B, int V) {
     if (B < 1 || V < 1) return 0;
-    const int64_t chunk = probs::chunk_of(B, V), chunks = (V + chunk - 1) / chunk;
-    if (B * chunks > kMaxGroups) return 0;
-    return up_to((size_t)B * sizeof(probs::Rec), 256) + up_to((size_t)(B * chunks) * sizeof(double), 256);
+    const int64_t cell = probs::cell_of(V), cells = (V + cell - 1) / cell;
+    if (B * cells > kMaxGroups) return 0;
+    return up_to((size_t)B * sizeof(probs::Rec), 256) + up_to((size_t)(B * cells) * sizeof(double), 256);
 }
 
 int spec_verify_probs(const void* draft_probs, int64_t draft_request_stride, int64_t draft_row_stride,
@@ -82,8 +82,9 @@ int spec_verify_probs(const void* draft_probs, int64_t draft_request_stride, int
     a.out_emitted = out_emitted;
     a.out_mass = out_resid_mass;
     a.out_status = out_status;
-    a.chunk = probs::chunk_of(B, V);
-    a.chunks = (int)(((int64_t)V + a.chunk - 1) / a.chunk);
+    a.cell = probs::cell_of(V);
+    a.cells = (int)(((int64_t)V + a.cell - 1) / a.cell);
+    a.per = probs::per_of(B, a.cells);
     a.recs = static_cast<probs::Rec*>(workspace);
     a.sums = reinterpret_cast<double*>(static_cast<char*>(workspace) + up_to((size_t)B * sizeof(probs::Rec), 256));
     probs::launch(a, dtype, stream);

@@ -1,5 +1,5 @@
 // Verification from given probabilities and random numbers: launch arguments and the cut of a
-// vocabulary row into chunks, shared by the C ABI and the kernels.
+// vocabulary row into cells, shared by the C ABI and the kernels.
 #pragma once
 
 #include "common.h"
@@ -9,7 +9,8 @@ namespace probs {
 
 constexpr int kThreads = 256;
 constexpr int kTile = kThreads * 8;  // elements one workgroup takes in one step (8 per thread)
-constexpr int kMaxChunks = 1024;     // chunk masses per request the second kernel scans at once
+constexpr int kMaxCells = 1024;      // cell masses per request the second kernel scans at once
+constexpr int kCellsAtOnce = 4;      // most cells a workgroup of the first takes
 constexpr int kOneLaunchV = 4 * kTile;
 
 // What the first kernel hands to the second for a request.
@@ -37,21 +38,21 @@ struct Args {
     int32_t* out_emitted;
     float* out_mass;
     uint32_t* out_status;
-    int chunk, chunks;  // elements per chunk (a multiple of kTile), chunks per row
-    double* sums;       // [B][chunks] chunk masses
-    Rec* recs;          // [B]
+    int cell, cells;  // elements per cell (a multiple of kTile), cells per row
+    int per;          // cells per workgroup of the first kernel
+    double* sums;     // [B][cells] cell masses
+    Rec* recs;        // [B]
 };
 
-// Chunk length: the whole row up to kOneLaunchV tokens (one launch then does all); one tile while that gives at most eight workgroups per compute unit or so, four
-// tiles beyond (fewer chunk masses and decisions for the same streaming), and for rows of more
-// than kMaxChunks of those whatever keeps kMaxChunks.
-inline int chunk_of(int B, int V) {
-    const int64_t tiles = ((int64_t)V + kTile - 1) / kTile;
-    if (V <= kOneLaunchV) return (int)(tiles * kTile);
-    int64_t t = (int64_t)B * tiles <= 2048 ? 1 : 4;
-    if (tiles > t * kMaxChunks) t = (tiles + kMaxChunks - 1) / kMaxChunks;
-    return (int)(t * kTile > 0x7fffffff - kTile ? 0x7fffffff / kTile * kTile : t * kTile);
+// A row is cut into cells whose masses the draw finds its place by: one tile each, up to kMaxCells
+// of them (longer rows: longer cells).
+inline int cell_of(int V) {
+    const int64_t tiles = ((int64_t)V + kTile - 1) / kTile, t = (tiles + kMaxCells - 1) / kMaxCells;
+    return (int)(t * kTile);
 }
+// Workgroups take one cell while that gives at most eight or so per compute unit, several beyond
+// (fewer scans for the same streaming).
+inline int per_of(int B, int cells) { return (int64_t)B * cells <= 2048 ? 1 : kCellsAtOnce; }
 
 void launch(const Args& a, int dtype, hipStream_t stream);
 

@@ -2,8 +2,8 @@
 // drawn from, and the draw by inverse CDF in token order.
 //
 // What bounds it: of each request's K + 1 pairs of rows only the pair of the first rejected
-// position (or the target's row after the last accepted token) is read, once, for the chunk
-// masses; the draw re-reads one chunk.  So the floor is two rows per request at HBM rate, and for
+// position (or the target's row after the last accepted token) is read, once, for the masses of its
+// cells; the draw re-reads one cell.  So the floor is two rows per request at HBM rate, and for
 // few requests the chain of dependent loads (token, its two probabilities, the row).
 //
 // Every workgroup of a request repeats the scan (K gathers, one wave) instead of waiting for a
@@ -139,9 +139,9 @@ __device__ __forceinline__ Row<T> row_of(const Args& a, int b, int k, int len, b
     return r;
 }
 
-// Mass of [lo, hi) (lo a multiple of kTile), in every thread.
+// The thread's part of the mass of [lo, hi) (lo a multiple of kTile).
 template <typename T>
-__device__ __forceinline__ double range_mass(const Row<T>& r, int lo, int hi, double* red) {
+__device__ __forceinline__ double part_of_mass(const Row<T>& r, int64_t lo, int64_t hi) {
     double s = 0.0;
     for (int64_t t = lo; t < hi; t += kTile) {
         const int64_t i = t + (int64_t)threadIdx.x * 8;
@@ -151,46 +151,98 @@ __device__ __forceinline__ double range_mass(const Row<T>& r, int lo, int hi, do
             s += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
         }
     }
-    return block_sum(s, red);
+    return s;
 }
 
-// The first token of [lo, hi) whose running mass, from `before` on, exceeds `at`; the last one with
-// mass where none does (the running mass here and the sums `at` comes from may differ in their
-// last bits); -1 where none has mass.
-template <typename T>
-__device__ __forceinline__ int pick(const Row<T>& r, int lo, int hi, double before, double at, double* red, int* found) {
-    double run = before;
-    if (threadIdx.x == 0) found[0] = 0x7fffffff, found[1] = -1;
-    for (int64_t t = lo; t < hi; t += kTile) {
-        const int64_t i = t + (int64_t)threadIdx.x * 8;
-        double w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (i < hi) r.eight((int)i, w);
-        double mine = 0.0;
-        int last = -1;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kAhead = kOneLaunchV / kTile;  // most tiles a draw holds at once
+
+struct DrawShared {
+    double red[kWaves];
+    double tot[kAhead][kWaves];
+    int hit[kWaves], last[kWaves];
+    int cell, found;
+    double ahead;
+};
+
+struct Pick {
+    int token;      // -1: no token of the range has mass
+    double total;   // mass of the range
+};
+
+// The first token of [lo, hi) whose running mass, from `before` on, exceeds `at` (WHOLE: exceeds
+// v times the range's own mass; the range is then at most A tiles); the last one with mass
+// where none does (the running mass here and the sums `at` comes from may differ in their last
+// bits).  A tiles are loaded at once, so that their loads do not wait for each other.
+template <typename T, bool WHOLE, int A>
+__device__ __forceinline__ Pick pick(const Row<T>& r, int lo, int hi, double before, double at_or_v, DrawShared& sh) {
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    double run = before, at = at_or_v, all = 0.0;
+    int last = -1;
+    for (int64_t t0 = lo; t0 < hi; t0 += A * kTile) {
+        double w[A][8], prior[A];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            mine += w[e];
-            if (w[e] > 0.0) last = (int)i + e;
-        }
-        double total;
-        const double prior = block_exclusive_scan(mine, red, &total);  // its barriers order `found` too
-        if (last >= 0) atomicMax(&found[1], last);
-        double c = run + prior;
-        int hit = -1;
+        for (int q = 0; q < A; ++q) {
+            const int64_t i = t0 + q * kTile + (int64_t)threadIdx.x * 8;
+            if (i < hi) {
+                r.eight((int)i, w[q]);
+            } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            c += w[e];
-            if (hit < 0 && w[e] > 0.0 && c > at) hit = (int)i + e;
+                for (int e = 0; e < 8; ++e) w[q][e] = 0.0;
+            }
         }
-        if (hit >= 0) atomicMin(&found[0], hit);
+        __syncthreads();  // the last round's (or caller's) words have been read
+#pragma unroll
+        for (int q = 0; q < A; ++q) {
+            const double mine = ((w[q][0] + w[q][1]) + (w[q][2] + w[q][3])) + ((w[q][4] + w[q][5]) + (w[q][6] + w[q][7]));
+            const double upto = wave_scan(mine, &prior[q]);
+            if (lane == kWave - 1) sh.tot[q][wave] = upto;
+        }
         __syncthreads();
-        if (found[0] != 0x7fffffff) break;
-        run += total;
+        if (WHOLE) {
+            all = 0.0;
+#pragma unroll
+            for (int q = 0; q < A; ++q)
+#pragma unroll
+                for (int v = 0; v < kWaves; ++v) all += sh.tot[q][v];
+            at = at_or_v * all;
+        }
+        int hit = 0x7fffffff, mine_last = -1;
+#pragma unroll
+        for (int q = 0; q < A; ++q) {
+            double c = run;
+#pragma unroll
+            for (int v = 0; v < kWaves; ++v) {
+                const double x = sh.tot[q][v];
+                if (v < wave) c += x;
+                run += x;
+            }
+            c += prior[q];
+            const int i = (int)(t0 + q * kTile) + (int)threadIdx.x * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                c += w[q][e];
+                if (w[q][e] > 0.0) {
+                    mine_last = i + e;
+                    if (hit == 0x7fffffff && c > at) hit = i + e;
+                }
+            }
+        }
+        hit = wave_min(hit);
+        mine_last = wave_max(mine_last);
+        if (lane == 0) {
+            sh.hit[wave] = hit;
+            sh.last[wave] = mine_last;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) {
+            hit = sh.hit[v] < hit ? sh.hit[v] : hit;
+            last = sh.last[v] > last ? sh.last[v] : last;
+        }
+        if (hit != 0x7fffffff) return Pick{hit, all};
     }
-    __syncthreads();
-    const int f = found[0], l = found[1];
-    __syncthreads();
-    return f != 0x7fffffff ? f : l;
+    return Pick{last, all};
 }
 
 __device__ __forceinline__ void emit(const Args& a, int b, int k, int t, double mass, uint32_t status) {
@@ -205,123 +257,150 @@ __device__ __forceinline__ void emit(const Args& a, int b, int k, int t, double 
             a.out_emitted[(size_t)b * (a.K + 1) + j] = t >= 0 && j < k ? a.tokens[(size_t)b * a.K + j] : (j == k ? t : -1);
 }
 
-// The draw of request b given its chunk masses (in LDS or global memory) by a whole workgroup.
+// t* of a request whose residual is empty: p >= q everywhere, so t* ~ q_k over the whole row (never
+// on a path that counts).
 template <typename T>
-__device__ __forceinline__ void draw(const Args& a, int b, int k, int len, uint32_t status, const double* sums, double* red, int* found) {
-    if (k < 0) {
-        emit(a, b, 0, -1, 0.0, status);
+__device__ __forceinline__ void draw_from_target(const Args& a, int b, const Decision& d, double v, DrawShared& sh) {
+    const Row<T> r = row_of<T>(a, b, d.k, d.len, false);
+    const double all = block_sum(part_of_mass(r, 0, a.V), sh.red);
+    if (!(all > 0.0 && all < __builtin_inf())) {
+        emit(a, b, 0, -1, 0.0, d.status | SPEC_ST_BAD_PROB);
         return;
     }
-    // running mass of the chunks, four neighbours per thread
+    emit(a, b, d.k, pick<T, false, 1>(r, 0, a.V, 0.0, v * all, sh).token, 0.0, d.status | kStEmptyResidual);
+}
+
+// The requests nothing is drawn for, given the mass of the row to draw from.
+__device__ __forceinline__ bool refused(const Args& a, int b, const Decision& d, double v, double total) {
+    uint32_t why = 0u;
+    if (d.k < 0) why = d.status;
+    else if (!(v >= 0.0 && v <= 1.0)) why = d.status | kStBadParam;
+    else if (!(total < __builtin_inf()) || (total == 0.0 && d.k >= d.len)) why = d.status | SPEC_ST_BAD_PROB;
+    if (why) emit(a, b, 0, -1, 0.0, why);
+    return why != 0u;
+}
+
+// The scan by the first wave, handed to the others.
+template <typename T>
+__device__ __forceinline__ Decision decide_for_all(const Args& a, int b, Decision* shared) {
+    if (threadIdx.x < kWave) {
+        const Decision d = decide<T>(a, b);
+        if (threadIdx.x == 0) *shared = d;
+    }
+    __syncthreads();
+    return *shared;
+}
+
+// Rows of at most kOneLaunchV tokens: one workgroup per request does all, the draw from the masses it
+// holds in registers (V = 1024: 5.0 us, 15 in two launches).
+template <typename T>
+__global__ __launch_bounds__(kThreads) void probs_whole_kernel(Args a) {
+    __shared__ DrawShared sh;
+    __shared__ Decision shared;
+    const int b = blockIdx.x;
+    const double v = random_at(a.v, a.u64, b);
+    const Decision d = decide_for_all<T>(a, b, &shared);
+    Pick p{-1, 0.0};
+    if (d.k >= 0) p = pick<T, true, kAhead>(row_of<T>(a, b, d.k, d.len, true), 0, a.V, 0.0, v, sh);
+    if (refused(a, b, d, v, p.total)) return;
+    if (p.total == 0.0) draw_from_target<T>(a, b, d, v, sh);
+    else emit(a, b, d.k, p.token, d.k < d.len ? p.total : 0.0, d.status);
+}
+
+// One workgroup per (`per` cells, request): the scan, then the cells' masses.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void probs_scan_kernel(Args a) {
+    __shared__ double red[kCellsAtOnce][kWaves];
+    __shared__ Decision shared;
+    const int groups = (a.cells + a.per - 1) / a.per, b = blockIdx.x / groups, c0 = blockIdx.x % groups * a.per;
+    const Decision d = decide_for_all<T>(a, b, &shared);
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    if (d.k >= 0) {
+        const Row<T> r = row_of<T>(a, b, d.k, d.len, true);
+#pragma unroll
+        for (int q = 0; q < kCellsAtOnce; ++q) {
+            if (q >= a.per) break;
+            const int64_t lo = (int64_t)(c0 + q) * a.cell, hi = lo + a.cell;
+            const double s = wave_sum(part_of_mass(r, lo, hi < a.V ? hi : a.V));
+            if (lane == 0) red[q][wave] = s;
+        }
+    }
+    __syncthreads();
+    const int q = threadIdx.x;
+    if (q < a.per && c0 + q < a.cells) {
+        double s = 0.0;
+        for (int w = 0; w < kWaves && d.k >= 0; ++w) s += red[q][w];
+        a.sums[(size_t)b * a.cells + c0 + q] = s;
+    }
+    if (threadIdx.x == 0 && c0 == 0) a.recs[b] = Rec{d.k, d.len, d.status, 0};
+}
+
+// One workgroup per request: the cell the draw falls into, then the token within it.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void probs_draw_kernel(Args a) {
+    __shared__ DrawShared sh;
+    const int b = blockIdx.x;
+    const Rec rec = a.recs[b];
+    const double v = random_at(a.v, a.u64, b);
+    // running mass of the cells, four neighbours per thread (at most kMaxCells)
     double s[4], mine = 0.0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int c = threadIdx.x * 4 + e;
-        s[e] = c < a.chunks ? sums[c] : 0.0;
+        s[e] = c < a.cells ? a.sums[(size_t)b * a.cells + c] : 0.0;
         mine += s[e];
     }
+    if (threadIdx.x == 0) {
+        sh.cell = 0x7fffffff;
+        sh.found = -1;
+    }
     double total;
-    const double before = block_exclusive_scan(mine, red, &total);
-    const double v = random_at(a.v, a.u64, b);
-    const bool rejected = k < len;
-    if (!(v >= 0.0 && v <= 1.0)) {
-        emit(a, b, 0, -1, 0.0, status | kStBadParam);
+    const double before = block_exclusive_scan(mine, sh.red, &total);
+    const Decision d{rec.k, rec.len, rec.status};
+    if (refused(a, b, d, v, total)) return;
+    if (total == 0.0) {
+        draw_from_target<T>(a, b, d, v, sh);
         return;
     }
-    if (!(total < __builtin_inf()) || (total == 0.0 && !rejected)) {
-        emit(a, b, 0, -1, 0.0, status | SPEC_ST_BAD_PROB);
-        return;
-    }
-    Row<T> r = row_of<T>(a, b, k, len, true);
-    int t;
-    if (total == 0.0) {  // p >= q everywhere: t* ~ q_k, over the whole row (never on a path that counts)
-        r = row_of<T>(a, b, k, len, false);
-        const double all = range_mass(r, 0, a.V, red);
-        if (!(all > 0.0 && all < __builtin_inf())) {
-            emit(a, b, 0, -1, 0.0, status | SPEC_ST_BAD_PROB);
-            return;
-        }
-        status |= kStEmptyResidual;
-        t = pick(r, 0, a.V, 0.0, v * all, red, found);
-    } else {
-        const double at = v * total;
-        // the chunk whose running mass first exceeds `at`, or the last one with mass
-        __syncthreads();
-        if (threadIdx.x == 0) found[0] = 0x7fffffff, found[1] = -1;
-        __syncthreads();
-        double c = before;
-        int hit = -1, last = -1;
+    // the cell whose running mass first exceeds v times the total, or the last one with mass
+    const double at = v * total;
+    double c = before;
+    int hit = -1, last = -1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            c += s[e];
-            if (s[e] > 0.0) {
-                last = threadIdx.x * 4 + e;
-                if (hit < 0 && c > at) hit = last;
-            }
+    for (int e = 0; e < 4; ++e) {
+        c += s[e];
+        if (s[e] > 0.0) {
+            last = threadIdx.x * 4 + e;
+            if (hit < 0 && c > at) hit = last;
         }
-        if (hit >= 0) atomicMin(&found[0], hit);
-        if (last >= 0) atomicMax(&found[1], last);
-        __syncthreads();
-        const int chunk = found[0] != 0x7fffffff ? found[0] : found[1];
-        // the thread that holds the chunk says what came before it
-        if (threadIdx.x == chunk / 4) {
-            double x = before;
-            for (int e = 0; e < 4; ++e)
-                if (threadIdx.x * 4 + e < chunk) x += s[e];
-            red[0] = x;
-        }
-        __syncthreads();
-        const double ahead = red[0];
-        __syncthreads();
-        const int64_t lo = (int64_t)chunk * a.chunk, hi = lo + a.chunk;
-        t = pick(r, (int)lo, (int)(hi < a.V ? hi : a.V), ahead, at, red, found);
     }
-    emit(a, b, k, t, rejected ? total : 0.0, status);
-}
-
-// One workgroup per (chunk, request): the scan, then the chunk's mass.  With one chunk per row the
-// same workgroup draws as well.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void probs_scan_kernel(Args a) {
-    __shared__ double red[kThreads / kWave];
-    __shared__ int found[2];
-    __shared__ Decision shared;
-    const int b = blockIdx.x / a.chunks, c = blockIdx.x % a.chunks;
-    if (threadIdx.x < kWave) {
-        const Decision d = decide<T>(a, b);
-        if (threadIdx.x == 0) shared = d;
+    if (hit >= 0) atomicMin(&sh.cell, hit);
+    if (last >= 0) atomicMax(&sh.found, last);
+    __syncthreads();
+    const int cell = sh.cell != 0x7fffffff ? sh.cell : sh.found;
+    if ((int)threadIdx.x == cell / 4) {  // the thread that holds the cell says what comes before it
+        double x = before;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if ((int)threadIdx.x * 4 + e < cell) x += s[e];
+        sh.ahead = x;
     }
     __syncthreads();
-    const Decision d = shared;
-    double s = 0.0;
-    if (d.k >= 0) {
-        const int64_t lo = (int64_t)c * a.chunk, hi = lo + a.chunk;
-        s = range_mass(row_of<T>(a, b, d.k, d.len, true), (int)lo, (int)(hi < a.V ? hi : a.V), red);
-    }
-    if (a.chunks == 1) {
-        draw<T>(a, b, d.k, d.len, d.status, &s, red, found);
-        return;
-    }
-    if (threadIdx.x == 0) {
-        a.sums[(size_t)b * a.chunks + c] = s;
-        if (c == 0) a.recs[b] = Rec{d.k, d.len, d.status, 0};
-    }
-}
-
-// One workgroup per request: the chunk the draw falls into, then the token within it.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void probs_draw_kernel(Args a) {
-    __shared__ double red[kThreads / kWave];
-    __shared__ int found[2];
-    const int b = blockIdx.x;
-    const Rec r = a.recs[b];
-    draw<T>(a, b, r.k, r.len, r.status, a.sums + (size_t)b * a.chunks, red, found);
+    const int64_t lo = (int64_t)cell * a.cell, hi = lo + a.cell;
+    const Row<T> r = row_of<T>(a, b, d.k, d.len, true);
+    const Pick p = pick<T, false, 1>(r, (int)lo, (int)(hi < a.V ? hi : a.V), sh.ahead, at, sh);
+    emit(a, b, d.k, p.token, d.k < d.len ? total : 0.0, d.status);
 }
 
 template <typename T>
 static void launch_type(const Args& a, hipStream_t stream) {
-    hipLaunchKernelGGL(probs_scan_kernel<T>, dim3((unsigned)a.chunks * (unsigned)a.B), dim3(kThreads), 0, stream, a);
-    if (a.chunks > 1) hipLaunchKernelGGL(probs_draw_kernel<T>, dim3((unsigned)a.B), dim3(kThreads), 0, stream, a);
+    if (a.V <= kOneLaunchV) {
+        hipLaunchKernelGGL(probs_whole_kernel<T>, dim3((unsigned)a.B), dim3(kThreads), 0, stream, a);
+        return;
+    }
+    const unsigned groups = (unsigned)((a.cells + a.per - 1) / a.per) * (unsigned)a.B;
+    hipLaunchKernelGGL(probs_scan_kernel<T>, dim3(groups), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL(probs_draw_kernel<T>, dim3((unsigned)a.B), dim3(kThreads), 0, stream, a);
 }
 
 void launch(const Args& a, int dtype, hipStream_t stream) {

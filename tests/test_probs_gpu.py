@@ -140,6 +140,14 @@ def test_strided_and_unaligned_rows(V):
     check(one, qd, tokens, rng.random((B, K)), rng.random(B))
 
 
+def test_a_row_longer_than_the_cells_of_one_tile():
+    """2.2 million tokens: cells of two tiles each."""
+    V = 2200003
+    g = torch.Generator().manual_seed(1)
+    q, p = (torch.rand((3, n, V), generator=g).cuda() ** 4 for n in (2, 1))
+    check(p, q, np.array([[5], [V - 1], [1 << 20]]), np.array([[1.0], [0.0], [1.0]]), np.array([0.25, 0.999999, 0.5]), lens=[1, 1, 1])
+
+
 def test_edges_of_the_random_numbers():
     q = torch.tensor([[[0.0, 0.25, 0.0, 0.75, 0.0], [0.0, 0.5, 0.5, 0.0, 0.0]]]).cuda().expand(6, 2, 5).contiguous()
     p = torch.tensor([[[0.0, 1.0, 0.0, 0.0, 0.0]]]).cuda().expand(6, 1, 5).contiguous()
