@@ -603,8 +603,8 @@ def spec_verify_probs(draft: Optional[torch.Tensor], target: torch.Tensor, token
         _whole("draft_lens", draft_lens, _I32, (B,))
     dev = target.get_device()
     if out is None:
-        k, tstar, status, mass = torch.empty((4, B), dtype=_I32, device=target.device).unbind()
-        out = ProbsOut(k, tstar, torch.empty((B, rows), dtype=_I32, device=target.device), mass.view(_F32), status)
+        k, tstar, status, mass = torch.empty(4, B, dtype=_I32, device=target.device).unbind()
+        out = ProbsOut(k, tstar, torch.empty(B, rows, dtype=_I32, device=target.device), mass.view(_F32), status)
     else:
         for name in ("k", "tstar", "status"):
             _whole(f"out.{name}", getattr(out, name), _I32, (B,))
@@ -645,8 +645,8 @@ def spec_tree_rows(tokens: torch.Tensor, parents: torch.Tensor, slots: torch.Ten
     if max_depth < 1:
         raise ValueError("max_depth must be at least 1")
     if out is None:
-        pos, app, length = torch.empty((3, B, N), dtype=_I32, device=tokens.device).unbind()
-        out = TreeRows(pos, app, torch.empty((B, N, max_depth), dtype=_I32, device=tokens.device), length)
+        pos, app, length = torch.empty(3, B, N, dtype=_I32, device=tokens.device).unbind()
+        out = TreeRows(pos, app, torch.empty(B, N, max_depth, dtype=_I32, device=tokens.device), length)
     else:
         for name in ("positions", "append_slots", "suffix_len"):
             _whole(f"out.{name}", getattr(out, name), _I32, shape)
@@ -742,7 +742,7 @@ def spec_kv_append(k: Optional[torch.Tensor], v: Optional[torch.Tensor], positio
         q_heads = q.shape[1]
         qs = _strides("q", q)
         if q_out is None:
-            q_out = torch.empty((T, q_heads, D), dtype=q.dtype, device=q.device)
+            q_out = torch.empty(T, q_heads, D, dtype=q.dtype, device=q.device)
         elif q_out.shape != q.shape or q_out.dtype is not q.dtype:
             raise ValueError("q_out must be like q")
         os = _strides("q_out", q_out)
@@ -813,14 +813,14 @@ def spec_prefix_attention(q: torch.Tensor, cache: KVCache, page_table: Optional[
     else:
         suffix_len = None
     if out is None:
-        out = torch.empty((R, Hq, D), dtype=q.dtype, device=q.device)
+        out = torch.empty(R, Hq, D, dtype=q.dtype, device=q.device)
     elif out.shape != q.shape or out.dtype is not q.dtype:
         raise ValueError("out must be like q")
     os = _strides("out", out)
     if lse is not None:
         _whole("lse", lse, _F32, (R, Hq))
     elif want_lse:
-        lse = torch.empty((R, Hq), dtype=_F32, device=q.device)
+        lse = torch.empty(R, Hq, dtype=_F32, device=q.device)
     if workspace is None:
         workspace = torch.empty(spec_prefix_attention_workspace_bytes(R, G, Hq, heads, D, pages * desc.page_size, S),
                                 dtype=_U8, device=q.device)

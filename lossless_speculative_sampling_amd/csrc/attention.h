@@ -60,8 +60,10 @@ struct Plan {
     size_t piece_o, piece_ml, suffix_o, suffix_ml, groups, bytes;  // offsets into the workspace
 };
 
-// Pieces: enough for two workgroups on every compute unit.
-constexpr int kPieces = 512;
+// Pieces: as many workgroups as are resident at once, two on every compute unit (three for the
+// largest tile).  More of them, measured up to 2048, cost more in their beginnings and ends than they
+// give in balance.
+inline int pieces_of(const Tile& t) { return t.mb * t.wq == 8 ? 768 : 512; }
 
 inline Plan plan_of(int R, int G, int q_heads, int heads, int D, int64_t max_prefix, int max_suffix) {
     const int per = q_heads / heads;
@@ -69,7 +71,7 @@ inline Plan plan_of(int R, int G, int q_heads, int heads, int D, int64_t max_pre
     p.tile = tile_of(R, G, per, D);
     // tiles of one cache head: at most one begun per group beyond the whole ones
     const int64_t tiles = (int64_t)R * per / p.tile.queries() + G;
-    p.want = (kPieces + heads - 1) / heads;
+    p.want = (pieces_of(p.tile) + heads - 1) / heads;
     p.slots = max_prefix ? (int)(p.want + tiles) : 0;
     const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t pieces = (size_t)p.slots * heads, q = p.tile.queries();

@@ -293,63 +293,109 @@ struct PlanShared {
     Piece piece;
 };
 
-// Piece number x of a cache head.  The stretch: the groups' tiles times lengths over the pieces
-// aimed at, less half a piece per tile for the stretches that end early.  The first workgroup
-// leaves every group's first piece and count for the join.
-template <int MT, int KT>
-__device__ __forceinline__ Piece find_piece(const Args& a, int x, bool leave, PlanShared& sh) {
-    long long work = 0, tiles = 0;
-    for (int g = threadIdx.x; g < a.G; g += kThreads) {
-        const int t = (rows_of(a, g).y * a.per + MT - 1) / MT;
-        work += (long long)t * prefix_of(a, g);
-        tiles += t;
-    }
-    work = block_sum(work, sh.red64);
-    tiles = block_sum(tiles, sh.red64);
+// What a group asks for, and where its pieces begin.
+struct Share {
+    int2 rows;
+    int len, tiles, n;  // prefix, tiles, stretches
+};
+
+__device__ __forceinline__ Share share_of(const Args& a, int g, int mt) {
+    Share s;
+    s.rows = rows_of(a, g);
+    s.len = prefix_of(a, g);
+    s.tiles = (s.rows.y * a.per + mt - 1) / mt;
+    s.n = 0;
+    return s;
+}
+
+// The stretch: the groups' tiles times lengths over the pieces aimed at, less half a piece per tile
+// for the stretches that end early.  (A little more than the quotient in any case: there is room for
+// `want` pieces and one per tile.)
+template <int KT>
+__device__ __forceinline__ int stretch_of(const Args& a, long long work, long long tiles) {
     long long parts = a.want - tiles / 2;
     if (parts < a.want / 4) parts = a.want / 4;
     if (parts < 1) parts = 1;
-    long long stretch = (work + parts - 1) / parts;
-    stretch = (stretch + KT - 1) / KT * KT;
-    if (stretch < KT) stretch = KT;
+    const float x = (float)work / (float)parts * 1.000001f + 1.0f;
+    const int most = 0x7fffffff - 2 * KT;
+    return (x < (float)most ? (int)x + KT - 1 : most) / KT * KT;
+}
+
+// Piece `k` of the group that `s` describes; its stretches are alike.
+template <int KT>
+__device__ __forceinline__ Piece piece_of(const Share& s, int g, int k) {
+    Piece p;
+    const int part = k / s.tiles;
+    const int64_t each = (((int64_t)s.len + s.n - 1) / s.n + KT - 1) / KT * KT;
+    const int64_t begin = part * each, end = begin + each;
+    p.g = g;
+    p.tile = k - part * s.tiles;
+    p.begin = (int)(begin < s.len ? begin : s.len);
+    p.end = (int)(end < s.len ? end : s.len);
+    p.first = s.rows.x;
+    p.rows = s.rows.y;
+    return p;
+}
+
+// Piece number x of a cache head.  The first workgroup leaves every group's first piece and count
+// for the join.  Up to 64 groups lie in a wave's lanes and every wave finds the piece for itself;
+// more take the workgroup and its barriers.
+template <int MT, int KT>
+__device__ __forceinline__ Piece find_piece(const Args& a, int x, bool leave, PlanShared& sh) {
+    if (a.G <= kWave) {
+        const int lane = threadIdx.x & (kWave - 1);
+        Share s{make_int2(0, 0), 0, 0, 0};
+        if (lane < a.G) s = share_of(a, lane, MT);
+        const int stretch = stretch_of<KT>(a, wave_sum((long long)s.tiles * s.len), wave_sum(s.tiles));
+        s.n = s.tiles ? (int)(((unsigned)s.len + stretch - 1u) / (unsigned)stretch) : 0;
+        int at;
+        wave_scan(s.tiles * s.n, &at);
+        if (leave && lane < a.G && threadIdx.x < kWave) a.groups[lane] = make_int2(at, s.n);
+        const uint64_t mine = __ballot(x >= at && x < at + s.tiles * s.n);
+        if (mine == 0) return Piece{-1, 0, 0, 0, 0, 0};
+        const int g = __builtin_ctzll(mine);
+        const Share t{make_int2(wave_bcast(s.rows.x, g), wave_bcast(s.rows.y, g)), wave_bcast(s.len, g), wave_bcast(s.tiles, g),
+                      wave_bcast(s.n, g)};
+        return piece_of<KT>(t, g, x - wave_bcast(at, g));
+    }
+    long long work = 0, tiles = 0;
+    for (int g = threadIdx.x; g < a.G; g += kThreads) {
+        const Share s = share_of(a, g, MT);
+        work += (long long)s.tiles * s.len;
+        tiles += s.tiles;
+    }
+    work = block_sum(work, sh.red64);
+    tiles = block_sum(tiles, sh.red64);
+    const int stretch = stretch_of<KT>(a, work, tiles);
     if (threadIdx.x == 0) sh.piece.g = -1;
     int base = 0;
     for (int g0 = 0; g0 < a.G; g0 += kThreads) {
         const int g = g0 + threadIdx.x;
-        int t = 0, n = 0, len = 0;
-        int2 rows = make_int2(0, 0);
-        if (g < a.G) {
-            rows = rows_of(a, g);
-            len = prefix_of(a, g);
-            t = (rows.y * a.per + MT - 1) / MT;
-            n = t ? (int)((len + stretch - 1) / stretch) : 0;
-        }
+        Share s{make_int2(0, 0), 0, 0, 0};
+        if (g < a.G) s = share_of(a, g, MT);
+        s.n = s.tiles ? (int)(((unsigned)s.len + stretch - 1u) / (unsigned)stretch) : 0;
         int all;
-        const int at = base + block_exclusive_scan(t * n, sh.red, &all);
-        if (g < a.G && leave) a.groups[g] = make_int2(at, n);
-        if (x >= at && x < at + t * n) {
-            const int part = (x - at) / t;
-            const int64_t each = ((len + n - 1) / n + KT - 1) / KT * KT;  // the group's stretches alike
-            const int64_t begin = part * each, end = begin + each;
-            sh.piece.g = g;
-            sh.piece.tile = (x - at) - part * t;
-            sh.piece.begin = (int)(begin < len ? begin : len);
-            sh.piece.end = (int)(end < len ? end : len);
-            sh.piece.first = rows.x;
-            sh.piece.rows = rows.y;
-        }
+        const int at = base + block_exclusive_scan(s.tiles * s.n, sh.red, &all);
+        if (g < a.G && leave) a.groups[g] = make_int2(at, s.n);
+        if (x >= at && x < at + s.tiles * s.n) sh.piece = piece_of<KT>(s, g, x - at);
         base += all;
     }
     __syncthreads();
-    return sh.piece;
+    const Piece p = sh.piece;
+    const auto one = [](int v) { return __builtin_amdgcn_readfirstlane(v); };  // scalar registers
+    return Piece{one(p.g), one(p.tile), one(p.begin), one(p.end), one(p.first), one(p.rows)};
 }
 
-// Keys a workgroup takes per step, as far as the registers that hold the next step's go.
-constexpr int keys_of(int dp) { return dp > 128 ? 32 : 64; }
+// Keys a workgroup takes per step, as far as the registers that hold the next step's go: 32 for heads
+// of 256, and for tiles of 128 queries, where the products bound the time and three workgroups per
+// compute unit instead of two are worth more (320 queries per cache head over 8192 keys 190 -> 143 us;
+// where reading bounds it, 128 queries over 6144, 112 -> 117 us).
+constexpr int keys_of(int dp, int mb, int wq) { return dp > 128 || (dp == 128 && mb * wq == 8) ? 32 : 64; }
+constexpr int groups_per_cu(int dp, int mb, int wq) { return dp == 128 && mb * wq == 8 ? 3 : 2; }
 
 template <typename T, typename C, int DP, int MB, int WQ>
 struct PieceLds {
-    static constexpr int KT = keys_of(DP);
+    static constexpr int KT = keys_of(DP, MB, WQ);
     static constexpr int kTileBytes = KT * DP * 2;
     static constexpr int kWK = 4 / WQ;
     // the waves over the same queries meet in the same memory at the end
@@ -430,8 +476,8 @@ __device__ __forceinline__ void prefix_piece(const Args& a, int index, char* lds
     char* kl = lds;
     char* vl = lds + L::kTileBytes;
 
-    leave(pc.begin, page_of(pc.begin), 0);
     int page = page_of(pc.begin + KT);
+    leave(pc.begin, page_of(pc.begin), 0);
     __syncthreads();
     load(0);
     leave(pc.begin + KT, page, 1);
@@ -634,7 +680,7 @@ __device__ __forceinline__ void suffix_wave(const Args& a, int64_t task, char* l
 }
 
 template <typename T, typename C, int DP, int MB, int WQ>
-__global__ __launch_bounds__(kThreads, 2) void attention_pieces_kernel(Args a) {
+__global__ __launch_bounds__(kThreads, groups_per_cu(DP, MB, WQ)) void attention_pieces_kernel(Args a) {
     constexpr int kSuffixBytes = 4 * 32 * DP * 2;
     constexpr int kPieceBytes = PieceLds<T, C, DP, MB, WQ>::kBytes;
     __shared__ __align__(16) char lds[kPieceBytes > kSuffixBytes ? kPieceBytes : kSuffixBytes];
