@@ -452,8 +452,8 @@ int spec_tree_rows(const int32_t* tree_tokens, const int32_t* tree_parents, cons
                    int32_t* out_append_slots, int32_t* out_suffix_slots, int32_t* out_suffix_len, hipStream_t stream);
 
 /* A paged cache of keys and values: k and v are [num_pages][page_size][heads][head_dim] with
- * head_dim contiguous and the other strides in elements, the same for both (so a cache with heads
- * outside tokens, or keys and values side by side in one buffer, is described as well).  Slot s is
+ * head_dim contiguous and the other strides in elements, not negative and the same for both (so a
+ * cache with heads outside tokens, or keys and values side by side in one buffer, is described as well).  Slot s is
  * token s % page_size of page s / page_size; num_pages * page_size < 2^31.
  * dtype SPEC_BF16, SPEC_FP16, or SPEC_E4M3 with k_scale and v_scale [heads] float (null: 1): the
  * key of head h is its 8-bit value times k_scale[h]. */
@@ -478,7 +478,7 @@ typedef struct {
  * g_i = clamp((n_i - low) / (high - low), 0, 1), f_i becomes f_i (g_i + (1 - g_i) / factor).
  * factor = 1 leaves all as they are; low = high takes g_i = (n_i >= low) (+inf: all stretched,
  * linear interpolation of positions).  rot_dim even and >= 2, base > 0, factor >= 1, low <= high,
- * original_len >= 1.  out [rot_dim / 2] host. */
+ * original_len >= 1; low and high may be +inf.  out [rot_dim / 2] host. */
 int spec_rope_frequencies(int rot_dim, double base, double factor, double low, double high, int original_len,
                           double* out);
 
@@ -491,7 +491,7 @@ enum { SPEC_ROPE_INTERLEAVED = 1 }; /* pairs (2i, 2i + 1); without it pairs (i, 
  * rounded once, to the output's type; an 8-bit cache holds (value / scale), clamped to its range.
  *   q        [T][q_heads][head_dim] (null: no queries), q_out likewise: q itself (in place, the
  *            same strides) or memory apart from it
- *   k, v     [T][heads][head_dim] (both null with a null cache: queries only)
+ *   k, v     [T][heads][head_dim], apart from the cache (both null with a null cache: queries only)
  *   dtype    SPEC_BF16 or SPEC_FP16, of q, q_out, k and v; a cache of that type or SPEC_E4M3
  *   strides  in elements, per token and per head; head_dim is contiguous
  *   positions [T] int32;  freqs [rot_dim / 2] double, device; rot_dim even, 0 (no rotation, freqs

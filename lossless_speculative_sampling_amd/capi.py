@@ -557,6 +557,16 @@ def _data(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _lend(stream, dev: int, *tensors):
+    """Tensors allocated here for a stream that the caller named: their memory is not given away before
+    that stream has passed the call."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 @dataclass
 class ProbsOut:
     k: torch.Tensor           # [B] int32
@@ -616,6 +626,8 @@ def spec_verify_probs(draft: Optional[torch.Tensor], target: torch.Tensor, token
         _workspace(workspace)
     _on_one_device(dev, (target, draft, tokens, accept_u, sample_v, draft_lens, out.k, out.tstar, out.emitted,
                          out.resid_mass, out.status, workspace))
+    if stream is not None:
+        _lend(stream, dev, workspace, out.k, out.tstar, out.emitted, out.resid_mass, out.status)
     _call("spec_verify_probs", dev, stream, _data(draft), ds[0], ds[1], target.data_ptr(), ts[0], ts[1], code, B, K, V,
           tokens.data_ptr(), _data(draft_lens), accept_u.data_ptr(), sample_v.data_ptr(),
           SPEC_FP64 if ut is _F64 else SPEC_FP32, flags, out.k.data_ptr(), out.tstar.data_ptr(), out.emitted.data_ptr(),
@@ -653,6 +665,8 @@ def spec_tree_rows(tokens: torch.Tensor, parents: torch.Tensor, slots: torch.Ten
         _whole("out.suffix_slots", out.suffix_slots, _I32, (B, N, max_depth))
     dev = tokens.get_device()
     _on_one_device(dev, (tokens, parents, slots, ctx_len, out.positions, out.append_slots, out.suffix_slots, out.suffix_len))
+    if stream is not None:
+        _lend(stream, dev, out.positions, out.append_slots, out.suffix_slots, out.suffix_len)
     _call("spec_tree_rows", dev, stream, tokens.data_ptr(), parents.data_ptr(), slots.data_ptr(), ctx_len.data_ptr(), B, N,
           max_depth, out.positions.data_ptr(), out.append_slots.data_ptr(), out.suffix_slots.data_ptr(),
           out.suffix_len.data_ptr())
@@ -761,6 +775,8 @@ def spec_kv_append(k: Optional[torch.Tensor], v: Optional[torch.Tensor], positio
         _whole("status", status, _I32, (T,))
     dev = lead.get_device()
     _on_one_device(dev, (lead, q_out, k, v, positions, slots, freqs, status, *of_cache))
+    if stream is not None:
+        _lend(stream, dev, q_out)
     _call("spec_kv_append", dev, stream, _data(q), qs[0], qs[1], _data(q_out), os[0], os[1], _data(k), ks[0], ks[1],
           _data(v), vs[0], vs[1], code, T, q_heads, heads, D, _data(positions), _data(slots), _data(freqs), rot, rscale,
           rflags, None if desc is None else ctypes.byref(desc), _data(status))
@@ -829,6 +845,8 @@ def spec_prefix_attention(q: torch.Tensor, cache: KVCache, page_table: Optional[
     dev = q.get_device()
     _on_one_device(dev, (q, cache.k, cache.v, cache.k_scale, cache.v_scale, page_table, prefix_len, row_start,
                          suffix_slots, suffix_len, out, lse, workspace))
+    if stream is not None:
+        _lend(stream, dev, workspace, out, lse)
     _call("spec_prefix_attention", dev, stream, q.data_ptr(), qs[0], qs[1], code, R, Hq, ctypes.byref(desc), G,
           row_start.data_ptr(), _data(page_table), pages, _data(prefix_len), _data(suffix_slots), S, _data(suffix_len),
           D ** -0.5 if scale is None else scale, out.data_ptr(), os[0], os[1], _data(lse), workspace.data_ptr(),

@@ -260,7 +260,8 @@ __device__ __forceinline__ int2 rows_of(const Args& a, int g) {
 __device__ __forceinline__ float factor_of(const Args& a, int kvh, bool* negate) {
     const float c = a.scale * (a.cache.k_scale ? a.cache.k_scale[kvh] : 1.0f) * kLog2e;
     *negate = c < 0.0f;
-    return fmaxf(fabsf(c), 1e-37f);
+    const float size = fabsf(c);
+    return size < 1e-37f ? 1e-37f : size;  // (NaN stays)
 }
 
 // 16 queries as the right operand of the first product: lane l has query l % 16, elements
@@ -723,7 +724,9 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(Args a, int mt
             const int tiles = (rows.y * a.per + mt - 1) / mt, tile = q / mt;
             at0 = ((int64_t)(span.x + tile) * a.heads + kvh) * mt + (q - tile * mt);
             step = (int64_t)tiles * a.heads * mt;
-            parts += span.y;
+            // (there is room for all of them as long as row_start does not decrease)
+            const int room = a.slots - span.x - tile;
+            parts += room <= 0 ? 0 : min(span.y, (room - 1) / tiles + 1);
         }
         const auto ml_of = [&](int p) { return p < first ? a.suffix_ml[pair] : a.piece_ml[at0 + (p - first) * step]; };
         const auto o_of = [&](int p) { return (p < first ? a.suffix_o + pair * a.D : a.piece_o + (at0 + (p - first) * step) * a.D) + d; };

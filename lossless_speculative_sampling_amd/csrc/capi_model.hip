@@ -20,11 +20,14 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 // A grid's threads are counted in 32 bits: at most this many workgroups of 256.
 constexpr int64_t kMaxGroups = (1ll << 24) - 1;
 constexpr int kMaxHeadDim = 1024;
+// Tokens of a vocabulary or a prefix: positions a few tiles past the end still fit in 32 bits.
+constexpr int64_t kMaxLen = 0x7fff0000;
 
 // What every user of a paged cache needs of its description; SPEC_OK or an error.
 int check_cache(const spec_kv_cache* c, int dtype) {
     if (!c || !c->k || !c->v || c->num_pages < 1 || c->page_size < 1 || c->heads < 1 || c->head_dim < 1) return SPEC_EINVAL;
     if ((int64_t)c->num_pages * c->page_size > 0x7fffffffll) return SPEC_EINVAL;
+    if (c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0) return SPEC_EINVAL;
     if (c->dtype != dtype && c->dtype != SPEC_E4M3) return SPEC_EDTYPE;
     return SPEC_OK;
 }
@@ -36,7 +39,7 @@ bool half_type(int dtype) { return dtype == SPEC_BF16 || dtype == SPEC_FP16; }
 extern "C" {
 
 size_t spec_verify_probs_workspace_bytes(int B, int V) {
-    if (B < 1 || V < 1) return 0;
+    if (B < 1 || V < 1 || V > kMaxLen) return 0;
     const int64_t cell = probs::cell_of(V), cells = (V + cell - 1) / cell;
     if (B * cells > kMaxGroups) return 0;
     return up_to((size_t)B * sizeof(probs::Rec), 256) + up_to((size_t)(B * cells) * sizeof(double), 256);
@@ -97,7 +100,7 @@ int spec_tree_rows(const int32_t* tree_tokens, const int32_t* tree_parents, cons
     if (!tree_tokens || !tree_parents || !node_slots || !ctx_len || !out_positions || !out_append_slots ||
         !out_suffix_slots || !out_suffix_len)
         return SPEC_EINVAL;
-    if (B < 1 || N < 1 || max_depth < 1 || max_depth == 0x7fffffff || B > kMaxGroups) return SPEC_EINVAL;
+    if (B < 1 || N < 1 || max_depth < 1 || N > kMaxLen || max_depth > kMaxLen || B > kMaxGroups) return SPEC_EINVAL;
     kv::RowsArgs a{tree_tokens, tree_parents, node_slots, ctx_len, B, N, max_depth, out_positions, out_append_slots,
                    out_suffix_slots, out_suffix_len};
     kv::launch_rows(a, stream);
@@ -107,15 +110,14 @@ int spec_tree_rows(const int32_t* tree_tokens, const int32_t* tree_parents, cons
 int spec_rope_frequencies(int rot_dim, double base, double factor, double low, double high, int original_len,
                           double* out) {
     if (!out || rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > kMaxHeadDim || original_len < 1) return SPEC_EINVAL;
-    if (!(base > 0.0) || !std::isfinite(base) || !(factor >= 1.0) || !std::isfinite(factor) || !(low <= high))
+    if (!(base > 0.0) || !std::isfinite(base) || !(factor >= 1.0) || !std::isfinite(factor) || !(low <= high) ||
+        low == -HUGE_VAL)
         return SPEC_EINVAL;
     const double two_pi = 6.283185307179586477;
     for (int i = 0; i < rot_dim / 2; ++i) {
         const double f = std::pow(base, -2.0 * i / rot_dim);
         const double n = original_len * f / two_pi;
-        double g;
-        if (low == high || std::isinf(low) || std::isinf(high)) g = n >= high ? 1.0 : (n < low ? 0.0 : (std::isinf(high) ? 0.0 : 1.0));
-        else g = std::fmin(std::fmax((n - low) / (high - low), 0.0), 1.0);
+        const double g = low == high ? (n >= low ? 1.0 : 0.0) : std::fmin(std::fmax((n - low) / (high - low), 0.0), 1.0);
         out[i] = f * (g + (1.0 - g) / factor);
     }
     return SPEC_OK;
@@ -143,6 +145,7 @@ int spec_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
         if (cache->heads != heads || cache->head_dim != head_dim) return SPEC_EINVAL;
         if (cache->dtype != SPEC_E4M3 && (!aligned(cache->k, 2) || !aligned(cache->v, 2))) return SPEC_EINVAL;
         a.cache = *cache;
+        if (cache->dtype != SPEC_E4M3) a.cache.k_scale = a.cache.v_scale = nullptr;
     }
     a.q = q;
     a.q_out = q_out;
@@ -180,8 +183,8 @@ int spec_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
 size_t spec_prefix_attention_workspace_bytes(int R, int G, int q_heads, int heads, int head_dim, int64_t max_prefix,
                                              int max_suffix) {
     if (R < 0 || G < 1 || heads < 1 || q_heads < heads || q_heads % heads != 0 || q_heads > (1 << 16)) return 0;
-    if (head_dim < 8 || head_dim > attn::kMaxD || head_dim % 8 != 0 || max_prefix < 0 || max_prefix > 0x7fffffffll ||
-        max_suffix < 0 || G > kMaxGroups || (int64_t)R * q_heads > 8 * kMaxGroups)
+    if (head_dim < 8 || head_dim > attn::kMaxD || head_dim % 8 != 0 || max_prefix < 0 || max_prefix > kMaxLen ||
+        max_suffix < 0 || G > kMaxGroups || (int64_t)R * q_heads > 4 * kMaxGroups)
         return 0;
     const attn::Plan p = attn::plan_of(R, G, q_heads, heads, head_dim, max_prefix, max_suffix);
     if ((int64_t)p.slots * heads + p.suffix_blocks > kMaxGroups) return 0;

@@ -120,7 +120,7 @@ def test_lengths_and_pages(page, prefix):
     Case(rows, prefix, [1, 0, 5, 33], 8, 2, 64, page=page, seed=page).check()
 
 
-@pytest.mark.parametrize("rows", [[1], [2] * 9, [17], [64, 1, 33], [200], [0, 4, 0, 0, 7, 0], [1] * 130])
+@pytest.mark.parametrize("rows", [[1], [2] * 9, [17], [64, 1, 33], [200], [0, 4, 0, 0, 7, 0], [1] * 64, [1] * 65, [1, 0, 2] * 150])
 def test_rows_per_group(rows):
     Case(rows, [90 + 13 * (i % 7) for i in range(len(rows))], [3, 1, 2], 16, 4, 128, seed=len(rows), pad=3).check()
 
@@ -197,6 +197,45 @@ def test_infinite_scores():
     c.v.view(-1, 1, 64)[torch.as_tensor(c.tokens_of(0)[65]), :, 5] = float("inf")
     out, _ = c.run()
     assert (out[:, :, 5] == math.inf).all() and torch.isfinite(out[:, :, 6]).all()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-30, 3.0])
+def test_factors_of_the_scores(scale):
+    c = Case([5], [150], [3, 0], 8, 2, 64, seed=12, size=0.5)
+    c.scale = scale
+    c.check()
+    c = Case([5], [150], [3, 0], 8, 2, 64, cache="e4m3", seed=13, size=0.5)
+    c.scale = scale
+    c.scales = [torch.tensor([-0.7, 0.0]), torch.tensor([-1.3, 0.5])]  # turned round, and nothing at all
+    c.check()
+
+
+def test_a_nan_stays_in_its_row():
+    """A query of NaN, and one that sees a NaN of its own, next to others in the same tile."""
+    c = Case([6, 3], [90, 70], [4, 2, 3], 8, 2, 64, seed=14)
+    ref, lref = (x.cpu() for x in c.run())
+    c.q[2, 3] = float("nan")
+    c.k.view(-1, 2, 64)[int(c.lists[7, 0])] = float("nan")
+    got, lse = (x.cpu() for x in c.run())
+    bad = torch.zeros(c.R, c.Hq, dtype=torch.bool)
+    bad[2, 3], bad[7] = True, True
+    assert got[bad].isnan().all() and lse[bad].isnan().all()
+    assert torch.equal(got[~bad], ref[~bad]) and torch.equal(lse[~bad], lref[~bad])
+
+
+def test_named_streams():
+    """The stream argument, as an object and as a handle, while the current stream is another."""
+    c = Case([9, 3], [700, 90], [5, 2], 16, 4, 128, seed=15)
+    ref = c.run()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        s = torch.cuda.Stream()
+        for stream in (s, s.cuda_stream):
+            got = c.run(stream=stream, workspace=None)
+            junk = torch.full((1 << 22,), float("nan"), device="cuda")  # takes memory given away too early
+            s.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, ref))
+            del junk
 
 
 def test_strides_and_layouts():

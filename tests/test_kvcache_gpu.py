@@ -179,6 +179,47 @@ def test_strided_views_in_place_and_queries_alone():
     assert capi.spec_kv_append(k[:0], v[:0], pos[:0], slots[:0], cache, rotary, q=q[:0]).shape == (0, Hq, D)
 
 
+def test_named_streams_graphs_and_outputs_given():
+    T, Hq, Hkv, D, page = 40, 4, 2, 64, 16
+    q, k, v, kc, vc = make(T, Hq, Hkv, D, torch.bfloat16, torch.bfloat16, page, 3)
+    rotary = capi.Rotary(torch.tensor(capi.spec_rope_frequencies(D), dtype=torch.float64, device="cuda"), interleaved=True)
+    g = torch.Generator().manual_seed(5)
+    pos = torch.randint(0, 9999, (T,), generator=g, dtype=torch.int32).cuda()
+    slots = torch.randperm(kc.shape[0] * page, generator=g)[:T].to(torch.int32).cuda()
+    tok, par = torch.randint(0, 9, (3, 50), generator=g, dtype=torch.int32).cuda(), (torch.arange(50, dtype=torch.int32) - 1).expand(3, 50).contiguous().cuda()
+    node, ctx = torch.randint(0, 999, (3, 50), generator=g, dtype=torch.int32).cuda(), torch.tensor([0, 7, 500], dtype=torch.int32, device="cuda")
+    ref = capi.spec_kv_append(k, v, pos, slots, capi.KVCache(kc, vc), rotary, q=q)
+    rows = capi.spec_tree_rows(tok, par, node, ctx, 50)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        c2 = capi.KVCache(kc.clone(), vc.clone())
+        torch.cuda.synchronize()
+        got = capi.spec_kv_append(k, v, pos, slots, c2, rotary, q=q, stream=stream)
+        r2 = capi.spec_tree_rows(tok, par, node, ctx, 50, stream=stream)
+        s.synchronize()
+        assert torch.equal(got, ref) and torch.equal(c2.k, kc) and torch.equal(c2.v, vc)
+        assert torch.equal(r2.suffix_slots, rows.suffix_slots) and torch.equal(r2.positions, rows.positions)
+    held = capi.KVCache(torch.zeros_like(kc), torch.zeros_like(vc))
+    out = torch.empty_like(q)
+    trees = capi.TreeRows(*[torch.empty_like(x) for x in (rows.positions, rows.append_slots, rows.suffix_slots, rows.suffix_len)])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        capi.spec_kv_append(k, v, pos, slots, held, rotary, q=q, q_out=out)
+        capi.spec_tree_rows(tok, par, node, ctx, 50, out=trees)
+    for i in range(4):
+        k.normal_()
+        pos.add_(13)
+        ctx.add_(1)
+        graph.replay()
+        torch.cuda.synchronize()
+        now = capi.KVCache(torch.zeros_like(kc), torch.zeros_like(vc))
+        want = capi.spec_kv_append(k, v, pos, slots, now, rotary, q=q)
+        assert torch.equal(out, want) and torch.equal(held.k, now.k) and torch.equal(held.v, now.v)
+        r2 = capi.spec_tree_rows(tok, par, node, ctx, 50)
+        assert torch.equal(trees.positions, r2.positions) and torch.equal(trees.suffix_slots, r2.suffix_slots)
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 2^32 elements: the last slots are written where they belong."""
     Hkv, D, page = 8, 128, 64

@@ -35,7 +35,7 @@ def test_verify_probs_workspace():
     f = capi.spec_verify_probs_workspace_bytes
     assert f(0, 10) == 0 and f(1, 0) == 0 and f(1 << 30, 1 << 30) == 0
     assert 0 < f(1, 1) <= f(16, 128256) <= f(512, 151936)
-    assert f(1, (1 << 31) - 1) < 1 << 20
+    assert f(1, (1 << 31) - 1) == 0 and 0 < f(1, 0x7fff0000) < 1 << 20
 
 
 def _cache(**kw):
@@ -94,7 +94,7 @@ def test_attention_errors(bad, rc):
 
 @pytest.mark.parametrize("bad,rc", [
     (dict(head_dim=60), -1), (dict(head_dim=264), -1), (dict(token_stride=130), -1), (dict(page_stride=1), -1), (dict(k=0x1008), -1),
-    (dict(v=0x1002), -1), (dict(dtype=3, k=0x1004), -1), (dict(heads=3), -1), (dict(dtype=4), -2)])
+    (dict(v=0x1002), -1), (dict(dtype=3, k=0x1004), -1), (dict(page_stride=-2048), -1), (dict(head_stride=-64), -1), (dict(heads=3), -1), (dict(dtype=4), -2)])
 def test_attention_cache_errors(bad, rc):
     assert _attend(cache=_cache(**bad)) == rc
 
@@ -134,8 +134,9 @@ def test_rope_frequencies_stretch_all_and_errors():
     plain = np.array(capi.spec_rope_frequencies(16, 10000.0))
     all_ = np.array(capi.spec_rope_frequencies(16, 10000.0, 4.0, math.inf, math.inf))
     np.testing.assert_allclose(all_, plain / 4, rtol=1e-15)
+    np.testing.assert_allclose(capi.spec_rope_frequencies(16, 10000.0, 4.0, 1.0, math.inf), plain / 4, rtol=1e-15)
     for bad in (dict(rot_dim=0), dict(rot_dim=3), dict(rot_dim=2048), dict(base=0.0), dict(base=math.inf), dict(factor=0.5),
-                dict(low=3.0, high=2.0), dict(low=math.nan), dict(original_len=0), dict(factor=math.nan)):
+                dict(low=3.0, high=2.0), dict(low=math.nan), dict(low=-math.inf), dict(original_len=0), dict(factor=math.nan)):
         with pytest.raises(capi.SpecError):
             capi.spec_rope_frequencies(**{"rot_dim": 8, **bad})
 

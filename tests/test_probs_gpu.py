@@ -192,6 +192,41 @@ def test_rows_where_nothing_is_left_and_bad_input():
     check(p2, q2, np.array([[3, 77]]), np.array([[0.9, 7.0]]), np.array([0.3]))
 
 
+def test_many_requests():
+    rng = np.random.default_rng(9)
+    p, q = rows_of(rng, 1, 2, 6)
+    B = 70000
+    pd, qd = (torch.as_tensor(x).float().cuda().expand(B, -1, -1) for x in (p, q))
+    tok = rng.integers(0, 6, (B, 2)).astype(np.int32)
+    u, v = rng.random((B, 2)), rng.random(B)
+    r = capi.spec_verify_probs(pd, qd, torch.as_tensor(tok).cuda(), torch.as_tensor(u).cuda(), torch.as_tensor(v).cuda())
+    some = np.concatenate([np.arange(200), np.arange(B - 200, B)])
+    ref = oracle(pd[:400].double().cpu().numpy(), qd[:400].double().cpu().numpy(), tok[some], u[some], v[some], None)
+    for name, key in (("k", "k"), ("tstar", "t"), ("emitted", "emitted"), ("status", "status")):
+        np.testing.assert_array_equal(getattr(r, name).cpu().numpy()[some], ref[key])
+
+
+def test_outputs_given_and_a_named_stream():
+    rng = np.random.default_rng(4)
+    p, q = rows_of(rng, 5, 3, 20000)
+    pd, qd = (torch.as_tensor(x).float().cuda() for x in (p, q))
+    tok = torch.as_tensor(rng.integers(0, 9, (5, 3)).astype(np.int32)).cuda()
+    u, v = torch.rand((5, 3), device="cuda"), torch.rand(5, device="cuda")
+    ref = capi.spec_verify_probs(pd, qd, tok, u, v)
+    i32 = lambda *n: torch.full(n, -9, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = capi.ProbsOut(i32(5), i32(5), i32(5, 4), torch.full((5,), -9.0, device="cuda"), i32(5))
+    ws = torch.full((capi.spec_verify_probs_workspace_bytes(5, 20000),), 0xAB, dtype=torch.uint8, device="cuda")  # not cleared
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        got = capi.spec_verify_probs(pd, qd, tok, u, v, workspace=ws, out=out, stream=stream)
+        alone = capi.spec_verify_probs(pd, qd, tok, u, v, stream=stream)
+        s.synchronize()
+        assert got is out
+        for name in ("k", "tstar", "emitted", "resid_mass", "status"):
+            assert torch.equal(getattr(out, name), getattr(ref, name)) and torch.equal(getattr(alone, name), getattr(ref, name))
+
+
 def test_outside_the_drafts_support():
     q = torch.tensor([[[0.5, 0.5, 0.0], [0.2, 0.3, 0.5]]] * 2).cuda()
     p = torch.tensor([[[1.0, 0.0, 0.0]]] * 2).cuda()
