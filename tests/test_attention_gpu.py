@@ -125,6 +125,25 @@ def test_rows_per_group(rows):
     Case(rows, [90 + 13 * (i % 7) for i in range(len(rows))], [3, 1, 2], 16, 4, 128, seed=len(rows), pad=3).check()
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 1), (64, 16, 2), (128, 6, 1), (120, 8, 1), (256, 8, 1)])
+@pytest.mark.parametrize("page", [1, 16, 24, 128])
+@pytest.mark.parametrize("prefix", [[1], [31, 32, 33, 95], [96, 97, 127, 200], [2049, 0, 700]])
+def test_many_queries(D, Hq, Hkv, page, prefix):
+    """Tiles of 128 queries: groups that fill one, two, or just begin another; whole prefixes and holes."""
+    rows = [(16, 17, 33, 21)[i % 4] for i in range(len(prefix))]
+    c = Case(rows, prefix, [2, 0], Hq, Hkv, D, page=page, seed=page + D, pad=1)
+    c.check()
+    c.table[0, 0] = -1
+    c.table[-1, c.table.shape[1] // 2] = c.k.shape[0]
+    flat = [x.view(-1, c.Hkv, c.D) for x in (c.k, c.v)]
+    used = torch.zeros(flat[0].shape[0], dtype=torch.bool)
+    for r in range(c.R - 1):
+        used[torch.as_tensor(c.tokens_of(r))] = True
+    for x in flat:
+        x[~used] = float("nan")
+    c.check()
+
+
 @pytest.mark.parametrize("suffix", [[1], [16, 17], [32, 33, 31], [0, 300, 1], [64, 65, 640]])
 def test_suffixes(suffix):
     Case([4, 2, 6], [40, 0, 129], suffix, 8, 2, 128, seed=len(suffix)).check()
