@@ -83,17 +83,18 @@ template <typename T>
 struct Raw<T, uint8_t> {
     typedef u32x2 type;
     static __device__ __forceinline__ s16x8 widen(u32x2 x) {
-        float f[8];
+        uint32_t y[4];
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[w], false);
-            const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[w], true);
-            f[4 * w] = lo[0];
-            f[4 * w + 1] = lo[1];
-            f[4 * w + 2] = hi[0];
-            f[4 * w + 3] = hi[1];
+            if constexpr (__is_same(T, __bf16)) {
+                y[2 * w] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[w], 1.0f, false));
+                y[2 * w + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[w], 1.0f, true));
+            } else {
+                y[2 * w] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[w], 1.0f, false));
+                y[2 * w + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[w], 1.0f, true));
+            }
         }
-        return narrow8<T>(f);
+        return __builtin_bit_cast(s16x8, u32x4{y[0], y[1], y[2], y[3]});
     }
 };
 

@@ -198,6 +198,20 @@ def test_what_lies_outside_does_not_matter(cache):
     c.check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_every_value_of_an_8_bit_cache(dtype):
+    """One key per row, so that the output is its value: all 256 patterns come through exactly."""
+    every = torch.arange(256, dtype=torch.int32).to(torch.uint8).view(torch.float8_e4m3fn)
+    for prefix in ([1], [0]):                        # read as a prefix, and from a list
+        c = Case([1], prefix, [1 - prefix[0]], 2, 1, 256, dtype, "e4m3", page=4, seed=1)
+        c.scales = [torch.ones(1), torch.ones(1)]
+        spot = int(c.tokens_of(0)[0])
+        c.v.view(-1, 1, 256)[spot, 0] = every
+        got = c.run()[0].cpu()[0].float()
+        want = every.float().expand(2, 256)
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(9), want.nan_to_num(9))
+
+
 def test_infinite_scores():
     c = Case([2], [20], [2], 2, 1, 64, seed=6)
     c.q[:, :, 0] = 1.0
