@@ -392,9 +392,10 @@ int saguaro_verify_cache_lookup_timed(const void* draft_logits, const void* targ
  * Verification from given probabilities
  * ------------------------------------------------------------------------------------------- */
 
-/* Bytes of scratch spec_verify_probs needs for B requests over V tokens (pure host function; 0
- * for sizes it rejects).  Every call writes what it reads of it, so it needs no clearing; one
- * workspace serves one call at a time (two captured graphs that may run at once need two). */
+/* Bytes of scratch spec_verify_probs needs for B requests over V tokens (pure host function); 0 where
+ * it needs none (V up to 8192; the workspace may then be null), and for sizes it rejects.  Every call
+ * writes what it reads of it, so it needs no clearing; one workspace serves one call at a time (two
+ * captured graphs that may run at once need two). */
 size_t spec_verify_probs_workspace_bytes(int B, int V);
 
 /* spec_verify_probs - the acceptance scan and the correction token of spec_verify ([SpS]

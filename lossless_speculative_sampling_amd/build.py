@@ -50,7 +50,7 @@ def scratch_users(report: str) -> dict[str, int]:
 # kernels whose resource report must be present (a missing report would let a spill through)
 EXPECTED_KERNELS = ("fast_count_kernel", "fast_resolve_kernel", "fast_diverge_kernel", "generic_unit_kernel",
                     "finalize_kernel", "cache_lookup_kernel", "signpost_kernel", "probs_whole_kernel", "probs_scan_kernel",
-                    "probs_draw_kernel", "tree_rows_kernel", "kv_append_kernel", "attention_pieces_kernel",
+                    "probs_draw_kernel", "tree_rows_kernel", "kv_append_kernel", "attention_plan_kernel", "attention_pieces_kernel",
                     "attention_join_kernel")
 
 

@@ -620,10 +620,11 @@ def spec_verify_probs(draft: Optional[torch.Tensor], target: torch.Tensor, token
             _whole(f"out.{name}", getattr(out, name), _I32, (B,))
         _whole("out.emitted", out.emitted, _I32, (B, rows))
         _whole("out.resid_mass", out.resid_mass, _F32, (B,))
-    if workspace is None:
-        workspace = torch.empty(spec_verify_probs_workspace_bytes(B, V), dtype=_U8, device=target.device)
-    else:
+    need = spec_verify_probs_workspace_bytes(B, V)
+    if workspace is not None:
         _workspace(workspace)
+    elif need:
+        workspace = torch.empty(need, dtype=_U8, device=target.device)
     _on_one_device(dev, (target, draft, tokens, accept_u, sample_v, draft_lens, out.k, out.tstar, out.emitted,
                          out.resid_mass, out.status, workspace))
     if stream is not None:
@@ -631,7 +632,7 @@ def spec_verify_probs(draft: Optional[torch.Tensor], target: torch.Tensor, token
     _call("spec_verify_probs", dev, stream, _data(draft), ds[0], ds[1], target.data_ptr(), ts[0], ts[1], code, B, K, V,
           tokens.data_ptr(), _data(draft_lens), accept_u.data_ptr(), sample_v.data_ptr(),
           SPEC_FP64 if ut is _F64 else SPEC_FP32, flags, out.k.data_ptr(), out.tstar.data_ptr(), out.emitted.data_ptr(),
-          out.resid_mass.data_ptr(), out.status.data_ptr(), workspace.data_ptr(), workspace.numel())
+          out.resid_mass.data_ptr(), out.status.data_ptr(), _data(workspace), 0 if workspace is None else workspace.numel())
     return out
 
 

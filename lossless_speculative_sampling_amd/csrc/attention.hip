@@ -295,12 +295,6 @@ struct Piece {
     int first, rows;          // the group's rows
 };
 
-struct PlanShared {
-    long long red64[kThreads / kWave];
-    int red[kThreads / kWave];
-    Piece piece;
-};
-
 // What a group asks for, and where its pieces begin.
 struct Share {
     int2 rows;
@@ -345,17 +339,48 @@ __device__ __forceinline__ Piece piece_of(const Share& s, int g, int k) {
     return p;
 }
 
-// Piece number x of a cache head.  The first workgroup leaves every group's first piece and count
-// for the join.  Up to 64 groups lie in a wave's lanes and every wave finds the piece for itself;
-// more take the workgroup and its barriers.
+__device__ __forceinline__ int stretches(const Share& s, int stretch) {
+    return s.tiles ? (int)(((unsigned)s.len + stretch - 1u) / (unsigned)stretch) : 0;
+}
+
+// Every group's first piece and count, for more groups than a wave has lanes.
 template <int MT, int KT>
-__device__ __forceinline__ Piece find_piece(const Args& a, int x, bool leave, PlanShared& sh) {
+__global__ __launch_bounds__(kThreads) void attention_plan_kernel(Args a) {
+    __shared__ long long red64[kThreads / kWave];
+    __shared__ int red[kThreads / kWave];
+    long long work = 0, tiles = 0;
+    for (int g = threadIdx.x; g < a.G; g += kThreads) {
+        const Share s = share_of(a, g, MT);
+        work += (long long)s.tiles * s.len;
+        tiles += s.tiles;
+    }
+    work = block_sum(work, red64);
+    tiles = block_sum(tiles, red64);
+    const int stretch = stretch_of<KT>(a, work, tiles);
+    int base = 0;
+    for (int g0 = 0; g0 < a.G; g0 += kThreads) {
+        const int g = g0 + threadIdx.x;
+        Share s{make_int2(0, 0), 0, 0, 0};
+        if (g < a.G) s = share_of(a, g, MT);
+        s.n = stretches(s, stretch);
+        int all;
+        const int at = base + block_exclusive_scan(s.tiles * s.n, red, &all);
+        if (g < a.G) a.groups[g] = make_int2(at, s.n);
+        base += all;
+    }
+}
+
+// Piece number x of a cache head, by every wave for itself.  Up to 64 groups lie in its lanes (the first
+// workgroup leaves every group's first piece and count for the join); more are planned by a launch of
+// their own, and the wave looks its group up, 64 ways at a time (2048 groups of 150 tokens: 597 us with
+// every workgroup and every row going through all groups, 381 so).
+template <int MT, int KT>
+__device__ __forceinline__ Piece find_piece(const Args& a, int x, bool leave) {
+    const int lane = threadIdx.x & (kWave - 1);
     if (a.G <= kWave) {
-        const int lane = threadIdx.x & (kWave - 1);
         Share s{make_int2(0, 0), 0, 0, 0};
         if (lane < a.G) s = share_of(a, lane, MT);
-        const int stretch = stretch_of<KT>(a, wave_sum((long long)s.tiles * s.len), wave_sum(s.tiles));
-        s.n = s.tiles ? (int)(((unsigned)s.len + stretch - 1u) / (unsigned)stretch) : 0;
+        s.n = stretches(s, stretch_of<KT>(a, wave_sum((long long)s.tiles * s.len), wave_sum(s.tiles)));
         int at;
         wave_scan(s.tiles * s.n, &at);
         if (leave && lane < a.G && threadIdx.x < kWave) a.groups[lane] = make_int2(at, s.n);
@@ -366,32 +391,24 @@ __device__ __forceinline__ Piece find_piece(const Args& a, int x, bool leave, Pl
                       wave_bcast(s.n, g)};
         return piece_of<KT>(t, g, x - wave_bcast(at, g));
     }
-    long long work = 0, tiles = 0;
-    for (int g = threadIdx.x; g < a.G; g += kThreads) {
-        const Share s = share_of(a, g, MT);
-        work += (long long)s.tiles * s.len;
-        tiles += s.tiles;
+    // the last group that begins at or before x
+    int lo = 0, n = a.G;
+    while (n > 1) {
+        const int step = (n + kWave - 1) / kWave;
+        const bool before = lane * step < n && a.groups[lo + lane * step].x <= x;
+        const int c = __popcll(__ballot(before)) - 1;  // (the first always does)
+        lo += c * step;
+        n = n - c * step < step ? n - c * step : step;
     }
-    work = block_sum(work, sh.red64);
-    tiles = block_sum(tiles, sh.red64);
-    const int stretch = stretch_of<KT>(a, work, tiles);
-    if (threadIdx.x == 0) sh.piece.g = -1;
-    int base = 0;
-    for (int g0 = 0; g0 < a.G; g0 += kThreads) {
-        const int g = g0 + threadIdx.x;
-        Share s{make_int2(0, 0), 0, 0, 0};
-        if (g < a.G) s = share_of(a, g, MT);
-        s.n = s.tiles ? (int)(((unsigned)s.len + stretch - 1u) / (unsigned)stretch) : 0;
-        int all;
-        const int at = base + block_exclusive_scan(s.tiles * s.n, sh.red, &all);
-        if (g < a.G && leave) a.groups[g] = make_int2(at, s.n);
-        if (x >= at && x < at + s.tiles * s.n) sh.piece = piece_of<KT>(s, g, x - at);
-        base += all;
-    }
-    __syncthreads();
-    const Piece p = sh.piece;
+    const int g = __builtin_amdgcn_readfirstlane(lo);
+    const int2 span = a.groups[g];
+    Share s = share_of(a, g, MT);
+    s.n = span.y;
     const auto one = [](int v) { return __builtin_amdgcn_readfirstlane(v); };  // scalar registers
-    return Piece{one(p.g), one(p.tile), one(p.begin), one(p.end), one(p.first), one(p.rows)};
+    const int k = x - one(span.x);
+    if (k >= one(s.tiles) * one(s.n)) return Piece{-1, 0, 0, 0, 0, 0};
+    const Share t{make_int2(one(s.rows.x), one(s.rows.y)), one(s.len), one(s.tiles), one(s.n)};
+    return piece_of<KT>(t, g, k);
 }
 
 // Keys a workgroup takes per step, as far as the registers that hold the next step's go: 32 for heads
@@ -419,13 +436,12 @@ __device__ __forceinline__ void prefix_piece(const Args& a, int index, char* lds
     constexpr int kLoads = KT * kChunks / kThreads;    // of K, and of V, per thread
     constexpr int kStep = kThreads / kChunks;          // keys between a thread's loads
     typedef typename Raw<T, C>::type raw;
-    __shared__ PlanShared plan;
     __shared__ int64_t offs[2][KT];        // where a key lies (a key that does not exist: at the start)
     __shared__ uint32_t exists[2][KT / 32];  // which keys exist
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wq = wave % WQ, wk = wave / WQ;
     const int kvh = index % a.heads;
-    const Piece pc = find_piece<MT, KT>(a, index / a.heads, index == 0, plan);
+    const Piece pc = find_piece<MT, KT>(a, index / a.heads, index == 0);
     if (pc.g < 0) return;
     const int M = pc.rows * a.per;
     bool negate;
@@ -579,19 +595,20 @@ __device__ __forceinline__ void prefix_piece(const Args& a, int index, char* lds
     }
 }
 
-// The group of row r, or -1: how many groups begin at or before it, counted by `width` lanes that
-// share the row (a power of two; `lane` < width).
+// The group of row r, or -1, looked up by `width` lanes that share the row (a power of two; `lane` <
+// width), as many ways at a time: the last group that begins at or before r, if it holds r.
 __device__ __forceinline__ int group_of(const Args& a, int r, int lane, int width) {
-    int n = 0;
-    for (int g0 = 0; g0 < a.G; g0 += width) {
-        const int g = g0 + lane;
-        int mine = g < a.G && a.row_start[g] <= r ? 1 : 0;
-        for (int s = 1; s < width; s <<= 1) mine += __shfl_xor(mine, s);
-        n += mine;
-        if (mine < width) break;
+    if (a.row_start[0] > r) return -1;
+    int lo = 0, n = a.G;
+    while (n > 1) {
+        const int step = (n + width - 1) / width;
+        const bool before = lane * step < n && a.row_start[lo + lane * step] <= r;
+        const uint64_t set = __ballot(before) >> ((threadIdx.x & (kWave - 1)) - lane);
+        const int c = __popcll(width < kWave ? set & ((1ull << width) - 1) : set) - 1;  // (the first always does)
+        lo += c * step;
+        n = n - c * step < step ? n - c * step : step;
     }
-    const int g = n - 1;
-    return g >= 0 && r < a.row_start[g + 1] ? g : -1;
+    return r < a.row_start[lo + 1] ? lo : -1;
 }
 
 // ------------------------------------------------------------------------------------------
@@ -788,6 +805,8 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(Args a, int mt
 
 template <typename T, typename C, int DP, int MB, int WQ>
 static void launch_tile(const Args& a, hipStream_t stream) {
+    if (a.slots && a.G > kWave)
+        hipLaunchKernelGGL((attention_plan_kernel<16 * MB * WQ, keys_of(DP, MB, WQ)>), dim3(1), dim3(kThreads), 0, stream, a);
     const unsigned blocks = (unsigned)(a.slots * a.heads + a.suffix_blocks);
     if (blocks)
         hipLaunchKernelGGL((attention_pieces_kernel<T, C, DP, MB, WQ>), dim3(blocks), dim3(kThreads), 0, stream, a);

@@ -39,7 +39,7 @@ bool half_type(int dtype) { return dtype == SPEC_BF16 || dtype == SPEC_FP16; }
 extern "C" {
 
 size_t spec_verify_probs_workspace_bytes(int B, int V) {
-    if (B < 1 || V < 1 || V > kMaxLen) return 0;
+    if (B < 1 || V <= probs::kOneLaunchV || V > kMaxLen) return 0;
     const int64_t cell = probs::cell_of(V), cells = (V + cell - 1) / cell;
     if (B * cells > kMaxGroups) return 0;
     return up_to((size_t)B * sizeof(probs::Rec), 256) + up_to((size_t)(B * cells) * sizeof(double), 256);
@@ -62,8 +62,12 @@ int spec_verify_probs(const void* draft_probs, int64_t draft_request_stride, int
     if (!aligned(target_probs, e) || (!flags && !aligned(draft_probs, e)) || !aligned(accept_u, u) || !aligned(sample_v, u))
         return SPEC_EINVAL;
     const size_t need = spec_verify_probs_workspace_bytes(B, V);
-    if (need == 0) return SPEC_EINVAL;
-    if (!workspace || !aligned(workspace, 8) || workspace_bytes < need) return SPEC_EWORKSPACE;
+    if (V > probs::kOneLaunchV) {
+        if (need == 0) return SPEC_EINVAL;
+        if (!workspace || !aligned(workspace, 8) || workspace_bytes < need) return SPEC_EWORKSPACE;
+    } else if (B > kMaxGroups) {
+        return SPEC_EINVAL;
+    }
     probs::Args a{};
     a.draft = flags ? nullptr : draft_probs;
     a.draft_req = draft_request_stride;
@@ -88,8 +92,10 @@ int spec_verify_probs(const void* draft_probs, int64_t draft_request_stride, int
     a.cell = probs::cell_of(V);
     a.cells = (int)(((int64_t)V + a.cell - 1) / a.cell);
     a.per = probs::per_of(B, a.cells);
-    a.recs = static_cast<probs::Rec*>(workspace);
-    a.sums = reinterpret_cast<double*>(static_cast<char*>(workspace) + up_to((size_t)B * sizeof(probs::Rec), 256));
+    if (need) {
+        a.recs = static_cast<probs::Rec*>(workspace);
+        a.sums = reinterpret_cast<double*>(static_cast<char*>(workspace) + up_to((size_t)B * sizeof(probs::Rec), 256));
+    }
     probs::launch(a, dtype, stream);
     return launched();
 }

@@ -125,6 +125,11 @@ def test_rows_per_group(rows):
     Case(rows, [90 + 13 * (i % 7) for i in range(len(rows))], [3, 1, 2], 16, 4, 128, seed=len(rows), pad=3).check()
 
 
+def test_thousands_of_groups():
+    n = 4500
+    Case([1] * n, [(7 * i) % 23 for i in range(n)], [1, 0, 2], 2, 1, 64, page=8, seed=21, pad=2).check()
+
+
 @pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 1), (64, 16, 2), (128, 6, 1), (120, 8, 1), (256, 8, 1)])
 @pytest.mark.parametrize("page", [1, 16, 24, 128])
 @pytest.mark.parametrize("prefix", [[1], [31, 32, 33, 95], [96, 97, 127, 200], [2049, 0, 700]])

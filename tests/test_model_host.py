@@ -14,7 +14,7 @@ OFF = ctypes.c_void_p(0x1001)
 
 
 def _probs(**kw):
-    a = dict(draft=FAKE, target=FAKE, dtype=0, B=2, K=3, V=100, tokens=FAKE, u=FAKE, v=FAKE, ut=0, flags=0, k=FAKE, t=FAKE,
+    a = dict(draft=FAKE, target=FAKE, dtype=0, B=2, K=3, V=10000, tokens=FAKE, u=FAKE, v=FAKE, ut=0, flags=0, k=FAKE, t=FAKE,
              ws=FAKE, n=1 << 20)
     a.update(kw)
     return capi.load().cdll.spec_verify_probs(a["draft"], 300, 100, a["target"], 400, 100, a["dtype"], a["B"], a["K"], a["V"],
@@ -26,7 +26,7 @@ def _probs(**kw):
     (dict(draft=None), -1), (dict(target=None), -1), (dict(tokens=None), -1), (dict(u=None), -1), (dict(v=None), -1),
     (dict(k=None), -1), (dict(t=None), -1), (dict(B=0), -1), (dict(K=0), -1), (dict(V=0), -1), (dict(flags=1), -1),
     (dict(flags=10), -1), (dict(dtype=3), -2), (dict(dtype=9), -2), (dict(ut=1), -2), (dict(target=OFF), -1),
-    (dict(draft=OFF), -1), (dict(u=OFF), -1), (dict(B=1 << 30), -1), (dict(ws=None), -3), (dict(n=10), -3), (dict(ws=OFF), -3)])
+    (dict(draft=OFF), -1), (dict(u=OFF), -1), (dict(B=1 << 30), -1), (dict(B=1 << 30, V=100), -1), (dict(ws=None), -3), (dict(n=10), -3), (dict(ws=OFF), -3)])
 def test_verify_probs_errors(bad, rc):
     assert _probs(**bad) == rc
 
@@ -34,7 +34,7 @@ def test_verify_probs_errors(bad, rc):
 def test_verify_probs_workspace():
     f = capi.spec_verify_probs_workspace_bytes
     assert f(0, 10) == 0 and f(1, 0) == 0 and f(1 << 30, 1 << 30) == 0
-    assert 0 < f(1, 1) <= f(16, 128256) <= f(512, 151936)
+    assert f(1, 1) == f(512, 8192) == 0 and 0 < f(1, 8193) <= f(16, 128256) <= f(512, 151936)
     assert f(1, (1 << 31) - 1) == 0 and 0 < f(1, 0x7fff0000) < 1 << 20
 
 
