@@ -23,8 +23,8 @@
 // the second product's operand, and nearly every step needs neither the exchange between lanes
 // nor the scaling of the output.
 // Bound by reading the cache once where a group has up to 64 or so queries per cache head (six rows
-// over 131071 tokens in e4m3: the pieces 58 us, 4.6 TB/s; 16 tokens' worth of queries over 16 prefixes of
-// 6144 in bf16: 83 us in all, 4.9 TB/s; a plain read reaches 5.6); by the products and the exponentials
+// over 131071 tokens in e4m3: the pieces 58 us, 4.6 TB/s; 16 groups of 16 queries per cache head over
+// 6144 tokens in bf16: 83 us in all, 4.9 TB/s; a plain read reaches 5.6); by the products and the exponentials
 // beyond (128 queries: 115 us for the same; 320 per cache head over 8192 tokens: 150 us, 570 TFLOP/s).
 // Matrix and vector instructions of two or three waves per SIMD share the time there: of 64 keys
 // against 32 queries a wave spends 1024 cycles in the matrix cores and about 1250 in the vector unit.

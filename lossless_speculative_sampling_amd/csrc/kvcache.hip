@@ -67,7 +67,7 @@ void launch_rows(const RowsArgs& a, hipStream_t stream) {
 
 // ------------------------------------------------------------------------------------------
 // Rotary positions and the append.  A copy in which pairs of elements turn, so bounded by HBM for
-// many tokens (16383 tokens with 32 query and 8 cache heads of 128 in bf16: 86 us, 4.7 TB/s, what a
+// many tokens (16383 tokens with 32 query and 8 cache heads of 128 in bf16: 84 us, 4.8 TB/s, what a
 // copy of 4 GiB reaches) and by the launch for few (16 tokens: 3.9 us).  One workgroup per token: its threads take the angles
 // first (each pair index once, for all heads): position * freq less its whole turns in fp64, because
 // an fp32 angle of a position around 10^6 is off by 0.06; sin and cos of the remainder then need
