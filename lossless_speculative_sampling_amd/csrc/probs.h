@@ -11,6 +11,7 @@ constexpr int kThreads = 256;
 constexpr int kTile = kThreads * 8;  // elements one workgroup takes in one step (8 per thread)
 constexpr int kMaxCells = 1024;      // cell masses per request the second kernel scans at once
 constexpr int kCellsAtOnce = 4;      // most cells a workgroup of the first takes
+constexpr size_t kCacheBytes = 256u << 20;  // the last cache before HBM
 constexpr int kOneLaunchV = 4 * kTile;
 
 // What the first kernel hands to the second for a request.

@@ -148,6 +148,22 @@ def test_a_row_longer_than_the_cells_of_one_tile():
     check(p, q, np.array([[5], [V - 1], [1 << 20]]), np.array([[1.0], [0.0], [1.0]]), np.array([0.25, 0.999999, 0.5]), lens=[1, 1, 1])
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_more_rows_than_the_caches_hold(dtype):
+    rng = np.random.default_rng(8)
+    B, V = (300, 131073) if dtype == "fp32" else (600, 131073)
+    p, q = rows_of(rng, 2, 2, V)
+    at = np.arange(B) % 2
+    pd, qd = (torch.as_tensor(x).to(DT[dtype]).cuda()[at] for x in (p, q))
+    tok = rng.integers(0, 99, (B, 2)).astype(np.int32)
+    u, v = rng.random((B, 2)), rng.random(B)
+    r = capi.spec_verify_probs(pd, qd, torch.as_tensor(tok).cuda(), torch.as_tensor(u).cuda(), torch.as_tensor(v).cuda())
+    some = np.concatenate([np.arange(8), np.arange(B - 8, B)])
+    ref = oracle(pd[some].double().cpu().numpy(), qd[some].double().cpu().numpy(), tok[some], u[some], v[some], None)
+    for name, key in (("k", "k"), ("tstar", "t"), ("emitted", "emitted"), ("status", "status")):
+        np.testing.assert_array_equal(getattr(r, name).cpu().numpy()[some], ref[key])
+
+
 def test_edges_of_the_random_numbers():
     q = torch.tensor([[[0.0, 0.25, 0.0, 0.75, 0.0], [0.0, 0.5, 0.5, 0.0, 0.0]]]).cuda().expand(6, 2, 5).contiguous()
     p = torch.tensor([[[0.0, 1.0, 0.0, 0.0, 0.0]]]).cuda().expand(6, 1, 5).contiguous()
