@@ -776,13 +776,13 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(Args a, int mt
                 float f[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x[e] = *reinterpret_cast<const f32x4*>(o_of(p + e * ways));
+                    x[e] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(o_of(p + e * ways)));
                     f[e] = ml_of(p + e * ways).x;
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o += x[e] * exp2_fast(f[e] - m);
             }
-            for (; p < parts; p += ways) o += *reinterpret_cast<const f32x4*>(o_of(p)) * exp2_fast(ml_of(p).x - m);
+            for (; p < parts; p += ways) o += __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(o_of(p))) * exp2_fast(ml_of(p).x - m);
         }
     }
     if (shared) {
