@@ -25,7 +25,7 @@
 // Bound by reading the cache once where a group has up to 64 or so queries per cache head (six rows
 // over 131071 tokens in e4m3: the pieces 54 us, 5.0 TB/s; 16 groups of 16 queries per cache head over
 // 6144 tokens in bf16: 73 us in all, 5.5 TB/s; a plain read reaches 5.6); by the products and the exponentials
-// beyond (128 queries: 112 us for the same; 320 per cache head over 8192 tokens: 150 us, 570 TFLOP/s).
+// beyond (128 queries: 104 to 108 us for the same; 320 per cache head over 8192 tokens: 150 us, 570 TFLOP/s).
 // Matrix and vector instructions of two or three waves per SIMD share the time there: of 64 keys
 // against 32 queries a wave spends 1024 cycles in the matrix cores and about 1250 in the vector unit.
 #include "attention.h"
@@ -486,24 +486,17 @@ __device__ __forceinline__ void prefix_piece(const Args& a, int index, char* lds
         }
     };
     // (of a key that does not exist the cache's first token is loaded: its score is masked, its value
-    // zeroed on the way into LDS).  Non-temporal but for the largest tile, whose groups may have several:
-    // a prefix is read once (512 single rows over up to 2000 tokens 598 -> 550 us, 16 groups of 16 queries
-    // 82 -> 73; with tiles of 128, 16 groups of 128 queries 112 -> 104, but 16 of 72 to 148 107 -> 115).
-    constexpr bool once = MB * WQ < 8;
+    // zeroed on the way into LDS).  Non-temporal: a prefix is read once, or by its group's few tiles at
+    // about the same time (512 single rows over up to 2000 tokens 598 -> 550 us, 16 groups of 16 queries
+    // 82 -> 73; 64 groups of 64 queries whose 100 MB the last cache holds, 32.1 -> 33.1).
     const char* kc = reinterpret_cast<const char*>(static_cast<const C*>(a.cache.k) + (int64_t)kvh * a.cache.head_stride + chunk0);
     const char* vc = reinterpret_cast<const char*>(static_cast<const C*>(a.cache.v) + (int64_t)kvh * a.cache.head_stride + chunk0);
     auto load = [&](int buf) {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const int64_t o = offs[buf][key0 + j * kStep];
-            const raw *k = reinterpret_cast<const raw*>(kc + o), *v = reinterpret_cast<const raw*>(vc + o);
-            if constexpr (once) {
-                kr[j] = __builtin_nontemporal_load(k);
-                vr[j] = __builtin_nontemporal_load(v);
-            } else {
-                kr[j] = *k;
-                vr[j] = *v;
-            }
+            kr[j] = __builtin_nontemporal_load(reinterpret_cast<const raw*>(kc + o));
+            vr[j] = __builtin_nontemporal_load(reinterpret_cast<const raw*>(vc + o));
         }
     };
     char* kl = lds;
