@@ -6,10 +6,10 @@
 // cells; the draw re-reads one cell.  So the floor is two rows per request at HBM rate, and for
 // few requests the chain of dependent loads (token, its two probabilities, the row).
 //
-// Measured: 512 requests of V = 151936 in bf16 70 us, the scan 62 (5.0 TB/s of the 5.6 a plain read of
+// Measured: 512 requests of V = 151936 in bf16 66 us, the scan 60 (5.2 TB/s of the 5.6 a plain read of
 // that size reaches) and the draw 7; 16 of V = 128256 in fp32 5.3 and 5.7 us; one of V = 1024 5.2 us.
-// More cells per workgroup (8, 16: 73, 77 us) and all of a workgroup's loads ahead of its sums (65 for
-// the scan) did not help, nor did cheaper arithmetic: it is bound by its reads.
+// More cells per workgroup (8, 16: 2% and 8% more) and all of a workgroup's loads ahead of its sums (5%
+// more) did not help, nor did cheaper arithmetic: it is bound by its reads.
 //
 // Every workgroup of a request repeats the scan (K gathers, one wave) instead of waiting for a
 // launch of its own that would publish it.
